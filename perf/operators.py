@@ -106,7 +106,8 @@ def work(case):
 def _rows_to_e4m3(x):
     """(codes as bytes, one fp32 scale per row): e4m3(x / scale) with scale = amax / 448, 1 for a row of zeros."""
     x = x.float()
-    scale = x.abs().amax(dim=1) / 448
+    most = x.abs().amax(dim=1)
+    scale = most / torch.full_like(most, 448)       # by a tensor: torch multiplies by a number's rounded reciprocal
     scale = torch.where(scale == 0, torch.ones_like(scale), scale)
     codes = (x / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
     return codes.view(torch.uint8), scale
