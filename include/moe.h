@@ -92,6 +92,40 @@ int moe_route(const moe_bf16* x, const moe_bf16* Wg, const float* bias, const fl
               void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
+ * Router with scored selection: sigmoid or softmax scores, a bias on the scores that balances the
+ * experts' load, groups of experts, and weights that may be renormalised and scaled.  Per token,
+ * from logits l_e:
+ *   s_e   = 1 / (1 + e^-l_e)  or  softmax(l)_e;   key_e = s_e + bias_e
+ *   the E experts form n_group groups of E / n_group consecutive ones; a group's value is its
+ *   largest key (MOE_GROUP_MAX) or the sum of its two largest (MOE_GROUP_TOP2); the topk_group
+ *   groups of largest value stay (ties -> lower group; n_group = 1: all experts stay)
+ *   idx   = the k largest keys among the groups that stay, descending (ties -> lower expert)
+ *   w_j   = scale * s_idx_j, or scale * s_idx_j / (sum of the k selected scores) if renormalise
+ * The order is that of keys computed in 64 bits.  Without a bias, and with n_group = 1 or
+ * MOE_GROUP_MAX, it is the order of the logits.
+ * Masks: an expert whose logit (for one token) or bias (for all) is -inf is never selected; where
+ * fewer than k experts are left, the last slots hold idx = -1 and w = 0, which moe_permute drops.  A
+ * token whose logits are all -inf (padding) is dropped whole.  A group in which only one expert
+ * is left has that expert's key as its value.  NaN or +inf in a logit or the bias sets
+ * MOE_ERR_CHECK and masks that expert.
+ * moe_route() with a bias adds it to the logits instead, and selects by logit + bias.
+ */
+enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum moe_group_score { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+typedef struct moe_route_params {
+    int score;        /* enum moe_score */
+    int n_group;      /* 1..32, divides E */
+    int topk_group;   /* 1..n_group; topk_group * (E / n_group) >= k */
+    int group_score;  /* enum moe_group_score */
+    int renormalise;  /* 0 or 1 */
+    float scale;      /* finite; multiplies the weights */
+} moe_route_params;
+/* Arguments as moe_route(), with params (a host struct, read during the call). */
+int moe_route_scored(const moe_bf16* x, const moe_bf16* Wg, const float* bias, const float* logits_in,
+                     const moe_route_params* params, int T, int d, int E, int k, float* logits_out,
+                     int32_t* idx, float* w, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
  * Dispatch ([EP-KV] §8 count / sort / pack; [EP-DS3] §2.1 bincount + capacity, §3.1 sort by
  * expert id): per-expert histogram, capacity in token order (per expert the first
  * `capacity` assignments by ascending token index are kept; capacity < 0 = unlimited),
@@ -173,6 +207,64 @@ int moe_layer_forward(const moe_bf16* x, const moe_bf16* Wg, const float* bias,
                       const moe_bf16* W1s, const moe_bf16* W3s, const moe_bf16* W2s, int f_shared,
                       int T, int d, int E, int k, int f, double capacity_factor, int cap_mode,
                       moe_bf16* out, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * The layer with scored routing: moe_layer_forward() / moe_layer_forward_w8() /
+ * moe_layer_forward_w8a8() / moe_layer_route_count() with moe_route_scored()'s selection in the place of
+ * moe_route()'s.  After moe_layer_route_count_scored(), moe_layer_finish() and the expert-parallel calls
+ * go on from the workspace as they do after moe_layer_route_count().  Same shapes and workspaces.
+ *   moe_layer_forward_scored_w8: fp8 experts; activations_fp8 = 1 takes moe_layer_forward_w8a8()'s
+ *   products (workspace moe_workspace_bytes_a8, d, f, f_shared multiples of 128), 0 moe_layer_forward_w8()'s.
+ */
+struct moe_w8_experts;
+int moe_layer_forward_scored(const moe_bf16* x, const moe_bf16* Wg, const float* bias,
+                             const moe_route_params* params,
+                             const moe_bf16* W1, const moe_bf16* W3, const moe_bf16* W2,
+                             const moe_bf16* W1s, const moe_bf16* W3s, const moe_bf16* W2s, int f_shared,
+                             int T, int d, int E, int k, int f, double capacity_factor, int cap_mode,
+                             moe_bf16* out, void* ws, size_t ws_bytes, moe_stream_t stream);
+int moe_layer_forward_scored_w8(const moe_bf16* x, const moe_bf16* Wg, const float* bias,
+                                const moe_route_params* params, const struct moe_w8_experts* routed,
+                                const struct moe_w8_experts* shared, int f_shared, int activations_fp8,
+                                int T, int d, int E, int k, int f, double capacity_factor, int cap_mode,
+                                moe_bf16* out, void* ws, size_t ws_bytes, moe_stream_t stream);
+int moe_layer_route_count_scored(const moe_bf16* x, const moe_bf16* Wg, const float* bias,
+                                 const moe_route_params* params, int f_shared,
+                                 int T, int d, int E, int k, int f, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Dense layer: the products around the routed experts (a projection into the residual stream, a dense
+ * feed-forward block) with everything that follows the product in its epilogue:
+ *   y = bf16( act(x W^T + bias) + residual )
+ *   MOE_ACT_SWIGLU: y = bf16( silu(x W^T + bias) * (x W_up^T + bias_up) + residual )
+ * fp32 from the accumulator to the one rounding.  silu(a) = a / (1 + e^-a); gelu(a) = a Phi(a);
+ * gelu_tanh(a) = a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) / 2.
+ *   x        [M, K] bf16
+ *   W        [N, K] bf16           one row per output
+ *   W_up     [N, K] bf16           MOE_ACT_SWIGLU only, else NULL
+ *   bias     [N] fp32 or NULL;     bias_up [N] fp32 or NULL (MOE_ACT_SWIGLU only)
+ *   residual [M, N] bf16 or NULL   may be y itself
+ *   y        [M, N] bf16           may not overlap x or the weights
+ * 1 <= M, N, K <= 2^24, K % 8 == 0; M and N are free.  No workspace: sums that are split over K
+ * are joined on chip, in a fixed order.
+ */
+enum moe_act {
+    MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4, MOE_ACT_SWIGLU = 5
+};
+int moe_linear(const moe_bf16* x, const moe_bf16* W, const moe_bf16* W_up, const float* bias, const float* bias_up,
+               const moe_bf16* residual, int M, int N, int K, int act, moe_bf16* y, moe_stream_t stream);
+
+/*
+ * The dense layer with fp8 weights and activations: W = e4m3(Wq) * s per row (as the experts' weights of
+ * moe_layer_forward_w8()); each row of x is quantised with the scale amax / 448 (as in
+ * moe_layer_forward_w8a8()), and the fp32 accumulator is multiplied by both scales before the epilogue.
+ *   Wq, Wq_up [N, K] uint8, s, s_up [N] fp32     (the _up pair: MOE_ACT_SWIGLU only, else NULL)
+ *   ws holds the codes and scales of x: moe_linear_workspace_bytes(M, K).  K % 16 == 0.
+ */
+int moe_linear_workspace_bytes(int M, int K, size_t* bytes);
+int moe_linear_w8a8(const moe_bf16* x, const uint8_t* Wq, const float* s, const uint8_t* Wq_up, const float* s_up,
+                    const float* bias, const float* bias_up, const moe_bf16* residual, int M, int N, int K, int act,
+                    moe_bf16* y, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
  * Optional stage markers for measurement.  Each non-NULL member is a cudaEvent_t that

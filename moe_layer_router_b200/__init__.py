@@ -31,6 +31,9 @@ MOE_ERR_CHECK = -7
 MOE_ERR_DEVICE = -8
 
 MOE_CAP_NONE, MOE_CAP_PER_TOKEN, MOE_CAP_PER_ASSIGNMENT = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_SWIGLU = range(6)
 
 # Names of the intermediates moe_layer_forward leaves in its workspace (moe_workspace_layout order).
 WS_NAMES = ["logits", "idx", "w", "counts_raw", "counts", "offsets", "dest", "src_token",
@@ -79,6 +82,34 @@ class moe_w8_experts(ctypes.Structure):
     _fields_ = [("W1q", _vp), ("W3q", _vp), ("W2q", _vp), ("s1", _vp), ("s3", _vp), ("s2", _vp)]
 
 
+class moe_route_params(ctypes.Structure):
+    """Selection of moe_route_scored: score, groups, renormalisation and scale of the weights."""
+    _fields_ = [("score", _i32), ("n_group", _i32), ("topk_group", _i32), ("group_score", _i32),
+                ("renormalise", _i32), ("scale", ctypes.c_float)]
+
+    def __init__(self, score=MOE_SCORE_SIGMOID, n_group=1, topk_group=1, group_score=MOE_GROUP_TOP2, renormalise=1,
+                 scale=1.0):
+        super().__init__(score, n_group, topk_group, group_score, renormalise, scale)
+
+
+_rp = ctypes.POINTER(moe_route_params)
+_lib.moe_route_scored.argtypes = [_vp, _vp, _vp, _vp, _rp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.moe_route_scored.restype = _i32
+_lib.moe_layer_forward_scored.argtypes = [_vp, _vp, _vp, _rp, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
+                                          _i32, _i32, _i32, _i32, _i32, _dbl, _i32, _vp, _vp, _sz, _vp]
+_lib.moe_layer_forward_scored.restype = _i32
+_lib.moe_layer_forward_scored_w8.argtypes = [_vp, _vp, _vp, _rp, ctypes.POINTER(moe_w8_experts),
+                                             ctypes.POINTER(moe_w8_experts), _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                             _dbl, _i32, _vp, _vp, _sz, _vp]
+_lib.moe_layer_forward_scored_w8.restype = _i32
+_lib.moe_layer_route_count_scored.argtypes = [_vp, _vp, _vp, _rp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _sz, _vp]
+_lib.moe_layer_route_count_scored.restype = _i32
+_lib.moe_linear.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp]
+_lib.moe_linear.restype = _i32
+_lib.moe_linear_workspace_bytes.argtypes = [_i32, _i32, ctypes.POINTER(_sz)]
+_lib.moe_linear_workspace_bytes.restype = _i32
+_lib.moe_linear_w8a8.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _sz, _vp]
+_lib.moe_linear_w8a8.restype = _i32
 _lib.moe_layer_forward_cached_w8.argtypes = [_vp, _vp, _vp, ctypes.POINTER(moe_w8_experts),
                                              ctypes.POINTER(moe_w8_experts), _i32, _vp,
                                              ctypes.POINTER(moe_w8_experts), _i32, _i32, _i32, _i32, _i32, _i32,
@@ -206,6 +237,13 @@ def moe_route(x, Wg, bias, logits_in, T, d, E, k, logits_out, idx, w, ws, stream
                           _ptr(idx), _ptr(w), _ptr(ws), _nbytes(ws), _stream(stream)), "moe_route")
 
 
+def moe_route_scored(x, Wg, bias, logits_in, params: moe_route_params, T, d, E, k, logits_out, idx, w, ws,
+                     stream=None) -> None:
+    _check(_lib.moe_route_scored(_ptr(x), _ptr(Wg), _ptr(bias), _ptr(logits_in),
+                                 ctypes.byref(params) if params is not None else None, T, d, E, k, _ptr(logits_out),
+                                 _ptr(idx), _ptr(w), _ptr(ws), _nbytes(ws), _stream(stream)), "moe_route_scored")
+
+
 def moe_permute(x, idx, T, d, E, k, capacity, counts_raw, counts, offsets, dest, src_token, x_perm, ws,
                 stream=None) -> None:
     _check(_lib.moe_permute(_ptr(x), _ptr(idx), T, d, E, k, int(capacity), _ptr(counts_raw), _ptr(counts),
@@ -240,6 +278,55 @@ def moe_layer_forward(x, Wg, bias, W1, W3, W2, W1s, W3s, W2s, f_shared, T, d, E,
     _check(_lib.moe_layer_forward(_ptr(x), _ptr(Wg), _ptr(bias), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(W1s),
                                   _ptr(W3s), _ptr(W2s), f_shared, T, d, E, k, f, float(capacity_factor), cap_mode,
                                   _ptr(out), _ptr(ws), _nbytes(ws), _stream(stream)), "moe_layer_forward")
+
+
+def moe_layer_forward_scored(x, Wg, bias, params: moe_route_params, W1, W3, W2, W1s, W3s, W2s, f_shared, T, d, E, k, f,
+                             capacity_factor, cap_mode, out, ws, stream=None) -> None:
+    _check(_lib.moe_layer_forward_scored(_ptr(x), _ptr(Wg), _ptr(bias),
+                                         ctypes.byref(params) if params is not None else None, _ptr(W1), _ptr(W3),
+                                         _ptr(W2), _ptr(W1s), _ptr(W3s), _ptr(W2s), f_shared, T, d, E, k, f,
+                                         float(capacity_factor), cap_mode, _ptr(out), _ptr(ws), _nbytes(ws),
+                                         _stream(stream)), "moe_layer_forward_scored")
+
+
+def moe_layer_forward_scored_w8(x, Wg, bias, params: moe_route_params, routed: dict, shared: Optional[dict], f_shared,
+                                activations_fp8, T, d, E, k, f, capacity_factor, cap_mode, out, ws,
+                                stream=None) -> None:
+    """routed / shared: dicts of W1q, W3q, W2q, s1, s3, s2 tensors (shared None without a shared expert)."""
+    q, qs = _w8(routed), _w8(shared)
+    _check(_lib.moe_layer_forward_scored_w8(_ptr(x), _ptr(Wg), _ptr(bias),
+                                            ctypes.byref(params) if params is not None else None, ctypes.byref(q),
+                                            ctypes.byref(qs) if qs is not None else None, f_shared,
+                                            int(bool(activations_fp8)), T, d, E, k, f, float(capacity_factor),
+                                            cap_mode, _ptr(out), _ptr(ws), _nbytes(ws), _stream(stream)),
+           "moe_layer_forward_scored_w8")
+
+
+def moe_layer_route_count_scored(x, Wg, bias, params: moe_route_params, f_shared, T, d, E, k, f, ws,
+                                 stream=None) -> None:
+    _check(_lib.moe_layer_route_count_scored(_ptr(x), _ptr(Wg), _ptr(bias),
+                                             ctypes.byref(params) if params is not None else None, f_shared, T, d, E,
+                                             k, f, _ptr(ws), _nbytes(ws), _stream(stream)),
+           "moe_layer_route_count_scored")
+
+
+def moe_linear(x, W, W_up, bias, bias_up, residual, M, N, K, act, y, stream=None) -> None:
+    """y = act(x W^T + bias) + residual; act MOE_ACT_SWIGLU takes W_up (and bias_up), the others None."""
+    _check(_lib.moe_linear(_ptr(x), _ptr(W), _ptr(W_up), _ptr(bias), _ptr(bias_up), _ptr(residual), M, N, K, act,
+                           _ptr(y), _stream(stream)), "moe_linear")
+
+
+def moe_linear_workspace_bytes(M: int, K: int) -> int:
+    out = _sz(0)
+    _check(_lib.moe_linear_workspace_bytes(M, K, ctypes.byref(out)), "moe_linear_workspace_bytes")
+    return int(out.value)
+
+
+def moe_linear_w8a8(x, Wq, s, Wq_up, s_up, bias, bias_up, residual, M, N, K, act, y, ws, stream=None) -> None:
+    """moe_linear with e4m3 weight bytes and one fp32 scale per weight row; x is quantised row by row into ws."""
+    _check(_lib.moe_linear_w8a8(_ptr(x), _ptr(Wq), _ptr(s), _ptr(Wq_up), _ptr(s_up), _ptr(bias), _ptr(bias_up),
+                                _ptr(residual), M, N, K, act, _ptr(y), _ptr(ws), _nbytes(ws), _stream(stream)),
+           "moe_linear_w8a8")
 
 
 STAGES = ["route", "topk", "permute", "gate_up", "down", "combine", "end"]   # timeline of one layer call

@@ -3,6 +3,7 @@
 // The host side never allocates device memory and never synchronises (except
 // moe_get_error).  Every launch goes to the caller's stream.
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -15,6 +16,8 @@
 #include "expert_cache.cuh"
 #include "expert_parallel.cuh"
 #include "act_quant.cuh"
+#include "linear.cuh"
+#include "route_scored.cuh"
 
 namespace moe {
 namespace {
@@ -371,6 +374,42 @@ int run_topk(const float* logits, int nsplit, float* logits_out, const float* bi
     else if (epl <= 16) MOE_TOPK(16);
     else MOE_TOPK(32);
 #undef MOE_TOPK
+    return launch_status();
+}
+
+int check_route_params(const moe_route_params* r, int E, int k) {
+    if (!r || (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) ||
+        (r->group_score != MOE_GROUP_MAX && r->group_score != MOE_GROUP_TOP2) ||
+        (r->renormalise != 0 && r->renormalise != 1) || !std::isfinite(r->scale))
+        return MOE_ERR_INVALID_ARG;
+    if (r->n_group < 1 || r->n_group > ROUTE_MAX_GROUPS || E % r->n_group || r->topk_group < 1 ||
+        r->topk_group > r->n_group || (long long)r->topk_group * (E / r->n_group) < k)
+        return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+// Scored selection on `logits`; nsplit, logits_out as for run_topk.
+int run_route_scored(const float* logits, int nsplit, float* logits_out, const float* bias,
+                     const moe_route_params& r, int T, int E, int k, int32_t* idx, float* w, cudaStream_t s) {
+    RouteScored p;
+    memset(&p, 0, sizeof(p));
+    p.logits = logits;
+    p.nsplit = nsplit;
+    p.split_stride = (long long)T * E;
+    p.logits_out = logits_out;
+    p.bias = bias;
+    p.T = T; p.E = E; p.k = k;
+    p.sigmoid = r.score == MOE_SCORE_SIGMOID;
+    p.n_group = r.n_group;
+    p.topk_group = r.topk_group;
+    p.top2 = r.group_score == MOE_GROUP_TOP2;
+    p.renorm = r.renormalise;
+    p.scale = r.scale;
+    p.by_logit = !bias && (r.n_group == 1 || !p.top2);
+    p.idx = idx;
+    p.w = w;
+    const int warps = route_f64_warps(E);
+    route_scored_f64_kernel<<<(unsigned)(((long long)T + warps - 1) / warps), warps * 32, (size_t)warps * E * 8, s>>>(p);
     return launch_status();
 }
 
@@ -898,6 +937,42 @@ int moe_route(const moe_bf16* x, const moe_bf16* Wg, const float* bias, const fl
     return run_topk(logits_in, 1, nullptr, bias, T, E, k, idx, w, s);
 }
 
+int moe_route_scored(const moe_bf16* x, const moe_bf16* Wg, const float* bias, const float* logits_in,
+                     const moe_route_params* params, int T, int d, int E, int k, float* logits_out, int32_t* idx,
+                     float* w, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    MOE_REQUIRE(T >= 1 && k >= 1 && k <= MAX_TOPK && E >= k && E <= 1024 && (long long)T * k < (1ll << 31),
+                MOE_ERR_SHAPE);
+    int rc = check_route_params(params, E, k);
+    if (rc != MOE_OK) return rc;
+    MOE_REQUIRE(idx && w, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(aligned16(idx) && aligned16(w) && aligned16(bias) && aligned16(logits_in) && aligned16(logits_out),
+                MOE_ERR_ALIGN);
+    const int ks = logits_in ? 1 : router_ksplit(T, d, E);
+    const size_t own = logits_out ? 0 : align256((size_t)T * E * 4);
+    if (!logits_in) {
+        MOE_REQUIRE(x && Wg, MOE_ERR_INVALID_ARG);
+        MOE_REQUIRE(d >= 64 && d % 64 == 0, MOE_ERR_SHAPE);
+        MOE_REQUIRE(aligned16(x) && aligned16(Wg), MOE_ERR_ALIGN);
+        const size_t need = own + (ks > 1 ? (size_t)ks * T * E * 4 : 0);
+        MOE_REQUIRE(need == 0 || (ws && ws_bytes >= need), MOE_ERR_WORKSPACE);
+        MOE_REQUIRE(aligned16(ws), MOE_ERR_ALIGN);
+    }
+    DeviceInfo* di;
+    if ((rc = device_info(&di)) != MOE_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (logits_in) {
+        if (logits_out && logits_out != logits_in &&
+            cudaMemcpyAsync(logits_out, logits_in, (size_t)T * E * 4, cudaMemcpyDeviceToDevice, s) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        return run_route_scored(logits_in, 1, nullptr, bias, *params, T, E, k, idx, w, s);
+    }
+    float* dst = logits_out ? logits_out : static_cast<float*>(ws);
+    float* part = ks > 1 ? reinterpret_cast<float*>(static_cast<char*>(ws) + own) : nullptr;
+    if ((rc = run_router_gemm(di, x, Wg, T, d, E, dst, part, ks, s)) != MOE_OK) return rc;
+    return ks > 1 ? run_route_scored(part, ks, dst, bias, *params, T, E, k, idx, w, s)
+                  : run_route_scored(dst, 1, nullptr, bias, *params, T, E, k, idx, w, s);
+}
+
 int moe_permute(const moe_bf16* x, const int32_t* idx, int T, int d, int E, int k, int64_t capacity,
                 int32_t* counts_raw, int32_t* counts, int32_t* offsets, int32_t* dest, int32_t* src_token,
                 moe_bf16* x_perm, void* ws, size_t ws_bytes, moe_stream_t stream) {
@@ -977,6 +1052,7 @@ enum { LAYER_ROUTE = 1, LAYER_COUNT = 2, LAYER_FINISH = 4, LAYER_PERMUTE = 8, LA
 //   LAYER_COUNT   histogram only: counts_raw          (no capacity)
 //   LAYER_PERMUTE histogram, capacity (with fill_base), permutation; stops there
 //   LAYER_FINISH  histogram, capacity (with fill_base), permutation, experts, combine
+// scored: the routing of moe_route_scored() instead of moe_route()'s.
 // Routed expert weights served from the expert cache (moe_layer_forward_cached[_w8]).  cp lists
 // the per-expert arrays to copy (device-usable source addresses, slot arrays); the GEMMs then
 // read the slots (bf16: W1/W3/W2 arguments of layer_phases; fp8: its W8Weights) through slot_of.
@@ -990,9 +1066,11 @@ int layer_phases(int phases, const moe_bf16* x, const moe_bf16* Wg, const float*
                  const moe_bf16* W3, const moe_bf16* W2, const moe_bf16* W1s, const moe_bf16* W3s, const moe_bf16* W2s,
                  int f_shared, int T, int d, int E, int k, int f, long long C, const int32_t* fill_base,
                  moe_bf16* out, void* ws, size_t ws_bytes, cudaStream_t s, const moe_stage_events* events,
-                 const W8Weights* w8 = nullptr, const CacheArgs* cache = nullptr, bool act8 = false) {
+                 const W8Weights* w8 = nullptr, const CacheArgs* cache = nullptr, bool act8 = false,
+                 const moe_route_params* scored = nullptr) {
     int rc = check_shape(T, d, E, k, f);
     if (rc != MOE_OK) return rc;
+    if (scored && (rc = check_route_params(scored, E, k)) != MOE_OK) return rc;
     MOE_REQUIRE(f_shared >= 0 && f_shared % 64 == 0, MOE_ERR_SHAPE);
     MOE_REQUIRE(x && ws, MOE_ERR_INVALID_ARG);
     if (phases & LAYER_ROUTE) MOE_REQUIRE(Wg, MOE_ERR_INVALID_ARG);
@@ -1049,8 +1127,10 @@ int layer_phases(int phases, const moe_bf16* x, const moe_bf16* Wg, const float*
         float* part = reinterpret_cast<float*>(base + L.router_part);
         if ((rc = run_router_gemm(di, x, Wg, T, d, E, logits, part, ks, s)) != MOE_OK) return rc;
         if (!mark(ev.topk)) return MOE_ERR_CUDA;
-        rc = ks > 1 ? run_topk(part, ks, logits, bias, T, E, k, idx, w, s)
-                    : run_topk(logits, 1, nullptr, bias, T, E, k, idx, w, s);
+        const float* lg = ks > 1 ? part : logits;
+        float* sums = ks > 1 ? logits : nullptr;
+        rc = scored ? run_route_scored(lg, ks, sums, bias, *scored, T, E, k, idx, w, s)
+                    : run_topk(lg, ks, sums, bias, T, E, k, idx, w, s);
         if (rc != MOE_OK) return rc;
     }
     // weight-only fp8: 1-SM tiles (its own kernel); bf16 and fp8 x fp8: 2-SM tiles for big experts
@@ -1146,10 +1226,149 @@ int layer_phases(int phases, const moe_bf16* x, const moe_bf16* Wg, const float*
     return mark(ev.end) ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// ------------------------------------------------------------------ dense layer
+
+constexpr int kLinearMax = 1 << 24;
+
+struct LinearArgs {
+    const void *x, *W, *W_up;                  // bf16, or e4m3 codes
+    const float *sx, *sw, *sw_up;              // e4m3: scales
+    const float *bias, *bias_up;
+    const moe_bf16* residual;
+    int M, N, K, act;
+    moe_bf16* y;
+};
+
+int check_linear(const void* x, const void* W, const void* W_up, const float* s, const float* s_up, bool f8,
+                 const float* bias, const float* bias_up, const moe_bf16* residual, int M, int N, int K, int act,
+                 const moe_bf16* y) {
+    if (M < 1 || N < 1 || K < 1 || M > kLinearMax || N > kLinearMax || K > kLinearMax || K % (f8 ? 16 : 8))
+        return MOE_ERR_SHAPE;
+    if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU || !x || !W || !y || (f8 && !s)) return MOE_ERR_INVALID_ARG;
+    const bool gated = act == MOE_ACT_SWIGLU;
+    if (gated != (W_up != nullptr) || (f8 && gated != (s_up != nullptr)) || (!gated && bias_up))
+        return MOE_ERR_INVALID_ARG;
+    if (static_cast<const void*>(y) == x || static_cast<const void*>(y) == W || static_cast<const void*>(y) == W_up)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(W) || !aligned16(W_up) || !aligned16(s) || !aligned16(s_up) || !aligned16(bias) ||
+        !aligned16(bias_up) || !aligned16(residual) || !aligned16(y))
+        return MOE_ERR_ALIGN;
+    return MOE_OK;
+}
+
+template <bool F8, bool GATED>
+int launch_linear_split(const LinearArgs& a, cudaStream_t s) {
+    LinearParams p;
+    memset(&p, 0, sizeof(p));
+    p.M = a.M; p.N = a.N; p.K = a.K; p.act = a.act;
+    p.bias = a.bias; p.bias_up = a.bias_up;
+    p.residual = reinterpret_cast<const __nv_bfloat16*>(a.residual);
+    p.y = reinterpret_cast<__nv_bfloat16*>(a.y);
+    p.sx = a.sx; p.sw = a.sw; p.sw_up = a.sw_up;
+    // token tiles of equal size (multiples of 16)
+    const int mt0 = (a.M + 255) / 256;
+    p.bn = ((a.M + mt0 - 1) / mt0 + 15) / 16 * 16;
+    p.mt = (a.M + p.bn - 1) / p.bn;
+    p.tmem_cols = p.bn <= 32 ? 32 : p.bn <= 64 ? 64 : p.bn <= 128 ? 128 : 256;
+    const int nt = (a.N + (GATED ? 63 : 127)) / (GATED ? 64 : 128);
+    const int nk = (a.K + (F8 ? 127 : 63)) / (F8 ? 128 : 64);
+    p.stages = 4;
+    p.split = 1;
+    const long long tiles = (long long)nt * p.mt;
+    if (tiles * p.split >= (1ll << 31)) return MOE_ERR_SHAPE;
+    (void)nk;
+    CUtensorMap mW, mWup, mX;
+    auto mk = [&](CUtensorMap* m, const void* base, uint64_t rows, uint32_t box) {
+        return F8 ? make_map_e4m3(m, base, a.K, rows, box) : make_map(m, base, a.K, rows, box);
+    };
+    int rc;
+    if ((rc = mk(&mW, a.W, a.N, GATED ? 64 : 128)) != MOE_OK) return rc;
+    if (GATED) {
+        if ((rc = mk(&mWup, a.W_up, a.N, 64)) != MOE_OK) return rc;
+    } else {
+        mWup = mW;
+    }
+    if ((rc = mk(&mX, a.x, a.M, p.bn)) != MOE_OK) return rc;
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        static bool attr_set[kMaxDevices] = {};
+        int dev = 0;
+        cudaGetDevice(&dev);
+        if (!attr_set[dev]) {
+            if (cudaFuncSetAttribute(linear_split_kernel<F8, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     GEMM_SMEM_MAX) != cudaSuccess)
+                return MOE_ERR_CUDA;
+            attr_set[dev] = true;
+        }
+    }
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((unsigned)(tiles * p.split));
+    cfg.blockDim = dim3(LIN_THREADS);
+    cfg.dynamicSmemBytes = linear_smem_bytes(p.stages, p.bn);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, linear_split_kernel<F8, GATED>, mW, mWup, mX, p) != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
+}
+
+template <bool F8>
+int run_linear(const LinearArgs& a, cudaStream_t s) {
+    return a.act == MOE_ACT_SWIGLU ? launch_linear_split<F8, true>(a, s) : launch_linear_split<F8, false>(a, s);
+}
+
+size_t linear_scale_offset(int M, int K) { return align256((size_t)M * K); }
+
 }  // namespace
 }  // namespace moe
 
 extern "C" {
+
+int moe_linear(const moe_bf16* x, const moe_bf16* W, const moe_bf16* W_up, const float* bias, const float* bias_up,
+               const moe_bf16* residual, int M, int N, int K, int act, moe_bf16* y, moe_stream_t stream) {
+    int rc = check_linear(x, W, W_up, nullptr, nullptr, false, bias, bias_up, residual, M, N, K, act, y);
+    if (rc != MOE_OK) return rc;
+    DeviceInfo* di;
+    if ((rc = device_info(&di)) != MOE_OK) return rc;
+    const LinearArgs a = {x, W, W_up, nullptr, nullptr, nullptr, bias, bias_up, residual, M, N, K, act, y};
+    return run_linear<false>(a, static_cast<cudaStream_t>(stream));
+}
+
+int moe_linear_workspace_bytes(int M, int K, size_t* bytes) {
+    MOE_REQUIRE(bytes, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(M >= 1 && M <= kLinearMax && K >= 1 && K <= kLinearMax && K % 16 == 0, MOE_ERR_SHAPE);
+    *bytes = linear_scale_offset(M, K) + (size_t)M * 4;
+    return MOE_OK;
+}
+
+int moe_linear_w8a8(const moe_bf16* x, const uint8_t* Wq, const float* s, const uint8_t* Wq_up, const float* s_up,
+                    const float* bias, const float* bias_up, const moe_bf16* residual, int M, int N, int K, int act,
+                    moe_bf16* y, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    int rc = check_linear(x, Wq, Wq_up, s, s_up, true, bias, bias_up, residual, M, N, K, act, y);
+    if (rc != MOE_OK) return rc;
+    MOE_REQUIRE(ws, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(aligned16(ws), MOE_ERR_ALIGN);
+    size_t need = 0;
+    moe_linear_workspace_bytes(M, K, &need);
+    MOE_REQUIRE(ws_bytes >= need, MOE_ERR_WORKSPACE);
+    DeviceInfo* di;
+    if ((rc = device_info(&di)) != MOE_OK) return rc;
+    uint8_t* xq = static_cast<uint8_t*>(ws);
+    float* sx = reinterpret_cast<float*>(xq + linear_scale_offset(M, K));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((rc = run_quant_h(x, nullptr, M, K, xq, sx, st)) != MOE_OK) return rc;
+    const LinearArgs a = {xq, Wq, Wq_up, sx, s, s_up, bias, bias_up, residual, M, N, K, act, y};
+    return run_linear<true>(a, st);
+}
 
 int moe_layer_forward_ex(const moe_bf16* x, const moe_bf16* Wg, const float* bias, const moe_bf16* W1,
                          const moe_bf16* W3, const moe_bf16* W2, const moe_bf16* W1s, const moe_bf16* W3s,
@@ -1318,6 +1537,46 @@ int moe_layer_route_count(const moe_bf16* x, const moe_bf16* Wg, const float* bi
     return layer_phases(LAYER_ROUTE | LAYER_COUNT, x, Wg, bias, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
                         f_shared, T, d, E, k, f, -1, nullptr, nullptr, ws, ws_bytes, static_cast<cudaStream_t>(stream),
                         nullptr);
+}
+
+int moe_layer_route_count_scored(const moe_bf16* x, const moe_bf16* Wg, const float* bias,
+                                 const moe_route_params* params, int f_shared, int T, int d, int E, int k, int f,
+                                 void* ws, size_t ws_bytes, moe_stream_t stream) {
+    MOE_REQUIRE(params, MOE_ERR_INVALID_ARG);
+    return layer_phases(LAYER_ROUTE | LAYER_COUNT, x, Wg, bias, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+                        f_shared, T, d, E, k, f, -1, nullptr, nullptr, ws, ws_bytes, static_cast<cudaStream_t>(stream),
+                        nullptr, nullptr, nullptr, false, params);
+}
+
+int moe_layer_forward_scored(const moe_bf16* x, const moe_bf16* Wg, const float* bias, const moe_route_params* params,
+                             const moe_bf16* W1, const moe_bf16* W3, const moe_bf16* W2, const moe_bf16* W1s,
+                             const moe_bf16* W3s, const moe_bf16* W2s, int f_shared, int T, int d, int E, int k, int f,
+                             double capacity_factor, int cap_mode, moe_bf16* out, void* ws, size_t ws_bytes,
+                             moe_stream_t stream) {
+    MOE_REQUIRE(cap_mode >= MOE_CAP_NONE && cap_mode <= MOE_CAP_PER_ASSIGNMENT && params, MOE_ERR_INVALID_ARG);
+    const long long C = moe_capacity(T, E, k, capacity_factor, cap_mode);
+    return layer_phases(LAYER_ROUTE | LAYER_FINISH, x, Wg, bias, W1, W3, W2, W1s, W3s, W2s, f_shared, T, d, E, k, f, C,
+                        nullptr, out, ws, ws_bytes, static_cast<cudaStream_t>(stream), nullptr, nullptr, nullptr, false,
+                        params);
+}
+
+int moe_layer_forward_scored_w8(const moe_bf16* x, const moe_bf16* Wg, const float* bias,
+                                const moe_route_params* params, const moe_w8_experts* routed,
+                                const moe_w8_experts* shared, int f_shared, int activations_fp8, int T, int d, int E,
+                                int k, int f, double capacity_factor, int cap_mode, moe_bf16* out, void* ws,
+                                size_t ws_bytes, moe_stream_t stream) {
+    MOE_REQUIRE(cap_mode >= MOE_CAP_NONE && cap_mode <= MOE_CAP_PER_ASSIGNMENT && params && routed &&
+                    (activations_fp8 == 0 || activations_fp8 == 1),
+                MOE_ERR_INVALID_ARG);
+    if (activations_fp8) MOE_REQUIRE(d % 128 == 0 && f % 128 == 0 && f_shared % 128 == 0, MOE_ERR_SHAPE);
+    const long long C = moe_capacity(T, E, k, capacity_factor, cap_mode);
+    W8Weights q = {routed->W1q, routed->W3q, routed->W2q,
+                   shared ? shared->W1q : nullptr, shared ? shared->W3q : nullptr, shared ? shared->W2q : nullptr,
+                   routed->s1, routed->s3, routed->s2,
+                   shared ? shared->s1 : nullptr, shared ? shared->s3 : nullptr, shared ? shared->s2 : nullptr};
+    return layer_phases(LAYER_ROUTE | LAYER_FINISH, x, Wg, bias, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+                        f_shared, T, d, E, k, f, C, nullptr, out, ws, ws_bytes, static_cast<cudaStream_t>(stream),
+                        nullptr, &q, nullptr, activations_fp8 != 0, params);
 }
 
 int moe_fill_base(const int32_t* all_counts, int G, int rank, int E, int32_t* fill_base, moe_stream_t stream) {
