@@ -5,15 +5,18 @@
 // the fp32 accumulator multiplied by both.  Everything between the product and the one rounding to
 // bf16 is in fp32.
 //
-// linear_split_kernel: the weights are the MMA's M side (D^T = W x^T): a tile is 128 weight rows by
-// `bn` tokens (a multiple of 16, at most 256), so a single token costs no padded 128-row tile, and the
-// K range of a tile is cut over the CTAs of a cluster, which join their partial sums through
-// distributed shared memory in rank order: no workspace, no atomics, the same result every time.
-// SwiGLU tiles take 64 rows of W and the same 64 rows of W_up.
+// linear_split_kernel: the weights are the MMA's M side (D^T = W x^T), so a single token costs no padded
+// 128-row tile.  A tile is 128 CG weight rows by `bn` tokens (a multiple of 16, at most 256), computed by
+// one CTA (CG = 1) or by a pair on two SMs (CG = 2, tcgen05 cta_group::2: each CTA holds 128 weight rows
+// and half of the tokens, which halves the token traffic from L2).  The K range of a tile is cut over
+// `split` such CTAs or pairs of one cluster, which join their partial sums through distributed shared
+// memory in rank order: no workspace, no atomics, the same result every time.  SwiGLU tiles take 64
+// rows of W and the same 64 rows of W_up per CTA.
 //
-// Warp roles (192 threads): warp 0 TMA producer, warp 1 tensor memory + MMA issuer, warps 2-5 move the
-// accumulator to shared memory (over the ring, idle by then) as fp32 [token][128]; then all threads
-// add the partial sums, apply the epilogue and store 16 bytes (8 outputs of a token) at a time.
+// Warp roles (256 threads): warp 0 TMA producer, warp 1 tensor memory + MMA issuer, warps 2-3 bring the
+// epilogue's operands into L2.  Then all eight warps move the accumulator (a lane per output, a column per
+// token) to shared memory as fp32 [slice][token][128], each token's sums to the rank of the cluster
+// that owns the token, and each rank adds the slices of its tokens, applies the epilogue and stores.
 #pragma once
 
 #include "grouped_gemm.cuh"
@@ -25,7 +28,7 @@ enum { LIN_NONE = 0, LIN_RELU = 1, LIN_SILU = 2, LIN_GELU = 3, LIN_GELU_TANH = 4
 
 constexpr int LIN_BM = 128;                        // weight rows per tile
 constexpr int LIN_A_BYTES = LIN_BM * 128;          // one stage of weights: 128-byte rows
-constexpr int LIN_THREADS = 192;
+constexpr int LIN_THREADS = 256;
 constexpr int LIN_MAX_STAGES = 8;
 constexpr int LIN_MAX_SPLIT = 8;                   // portable cluster size
 
@@ -34,6 +37,7 @@ struct LinearParams {
     int bn;        // tokens per tile
     int mt;        // token tiles
     int stages, split;
+    int own_part;  // 1: the partial sums have shared memory of their own
     int tmem_cols; // power of two >= max(bn, 32)
     int act;
     const float *bias, *bias_up;
@@ -42,8 +46,11 @@ struct LinearParams {
     const float *sx, *sw, *sw_up;                  // F8 scales
 };
 
-__host__ __device__ constexpr int linear_smem_bytes(int stages, int bn) {
-    return stages * (LIN_A_BYTES + bn * 128) + 1024 + 256;
+// Partial sums of a CTA: `split` slices of ceil(ntok / split) tokens, at most bn + split - 1 rows.
+__host__ __device__ constexpr int linear_part_bytes(int bn, int split) { return (bn + split) * LIN_BM * 4; }
+// x_rows: token rows that one CTA loads per stage (bn / CG)
+__host__ __device__ constexpr int linear_smem_bytes(int stages, int x_rows, int own_part_bytes) {
+    return stages * (LIN_A_BYTES + x_rows * 128) + own_part_bytes + 1024 + 256;
 }
 
 // Activation of a pre-activation z (not SwiGLU).  gelu: z times the normal distribution function,
@@ -60,48 +67,195 @@ __device__ __forceinline__ float linear_act(int act, float z) {
     }
 }
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster_f1(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-__device__ __forceinline__ float ld_cluster_f1(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+// act of eight values; the branch on act is taken once
+__device__ __forceinline__ void linear_act8(int act, float (&z)[8]) {
+    switch (act) {
+        case LIN_RELU:
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = linear_act(LIN_RELU, z[i]);
+            break;
+        case LIN_SILU:
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = linear_act(LIN_SILU, z[i]);
+            break;
+        case LIN_GELU:
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = linear_act(LIN_GELU, z[i]);
+            break;
+        case LIN_GELU_TANH:
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = linear_act(LIN_GELU_TANH, z[i]);
+            break;
+        default: break;
+    }
 }
 
-// tcgen05 shapes: M = 128, N = bn; tensor maps: W / W_up with boxes of 128 rows (SwiGLU: 64), x with
-// boxes of bn rows.  grid = tiles * split, cluster = split CTAs of one tile.
+__device__ __forceinline__ float4 f4_or(const float* p, bool on, float v) {
+    return on ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(v, v, v, v);
+}
+
+__device__ __forceinline__ void bf16x4_to_f32(const uint2& v, float* f) {
+    f[0] = __uint_as_float(v.x << 16);
+    f[1] = __uint_as_float(v.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.y << 16);
+    f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+
+// The outputs of one of 256 epilogue threads, with their bias and scales: where rows of y are 8-byte aligned
+// (N % 4 == 0), 16 threads share a token and thread i has outputs 4 i .. 4 i + 3 and (not GATED)
+// 64 + 4 i .. 64 + 4 i + 3 of the CTA's 128 (GATED: 64).
 template <bool F8, bool GATED>
+struct LinearCols {
+    int f, na, nb;
+    bool oka, okb;
+    float4 ba, bb, wa, wb;
+    __device__ __forceinline__ void load(const LinearParams& p, int tid, int n0, int nout) {
+        f = (tid & 15) * 4;
+        na = n0 + f;
+        nb = GATED ? na : na + 64;
+        oka = f < nout;
+        okb = GATED ? oka : f + 64 < nout;
+        ba = f4_or(p.bias + na, p.bias != nullptr && oka, 0.0f);
+        bb = GATED ? f4_or(p.bias_up + nb, p.bias_up != nullptr && okb, 0.0f)
+                   : f4_or(p.bias + nb, p.bias != nullptr && okb, 0.0f);
+        wa = f4_or(p.sw + na, F8 && oka, 1.0f);
+        wb = GATED ? f4_or(p.sw_up + nb, F8 && okb, 1.0f) : f4_or(p.sw + nb, F8 && okb, 1.0f);
+    }
+    __device__ __forceinline__ void residual(const LinearParams& p, long long token, uint2& ra, uint2& rb) const {
+        ra = rb = make_uint2(0u, 0u);
+        if (p.residual) {
+            const __nv_bfloat16* r = p.residual + token * p.N;
+            if (oka) ra = *reinterpret_cast<const uint2*>(r + na);
+            if (!GATED && okb) rb = *reinterpret_cast<const uint2*>(r + nb);
+        }
+    }
+    // One token: its SPLIT partial sums at `part` (fp32 [128], `stride` apart) added in slice order, the
+    // epilogue, the store.
+    template <int SPLIT>
+    __device__ __forceinline__ void finish(const LinearParams& p, const float* part, int stride, long long token,
+                                           const uint2& ra, const uint2& rb) const {
+        float z[8];
+#pragma unroll
+        for (int r = 0; r < SPLIT; ++r) {
+            const float4 a = *reinterpret_cast<const float4*>(part + r * stride + f);
+            const float4 b = *reinterpret_cast<const float4*>(part + r * stride + 64 + f);
+            if (r == 0) {
+                z[0] = a.x; z[1] = a.y; z[2] = a.z; z[3] = a.w;
+                z[4] = b.x; z[5] = b.y; z[6] = b.z; z[7] = b.w;
+            } else {
+                z[0] += a.x; z[1] += a.y; z[2] += a.z; z[3] += a.w;
+                z[4] += b.x; z[5] += b.y; z[6] += b.z; z[7] += b.w;
+            }
+        }
+        if (F8) {
+            const float sx = __ldg(p.sx + token);
+            z[0] *= sx * wa.x; z[1] *= sx * wa.y; z[2] *= sx * wa.z; z[3] *= sx * wa.w;
+            z[4] *= sx * wb.x; z[5] *= sx * wb.y; z[6] *= sx * wb.z; z[7] *= sx * wb.w;
+        }
+        z[0] += ba.x; z[1] += ba.y; z[2] += ba.z; z[3] += ba.w;
+        z[4] += bb.x; z[5] += bb.y; z[6] += bb.z; z[7] += bb.w;
+        if (GATED) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = swiglu_f32(z[i], z[i + 4]);
+        } else {
+            linear_act8(p.act, z);
+        }
+        if (p.residual) {
+            float res[8];
+            bf16x4_to_f32(ra, res);
+            bf16x4_to_f32(rb, res + 4);
+#pragma unroll
+            for (int i = 0; i < (GATED ? 4 : 8); ++i) z[i] += res[i];
+        }
+        __nv_bfloat16* y = p.y + token * p.N;
+        if (oka) *reinterpret_cast<uint2*>(y + na) = make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
+        if (!GATED && okb)
+            *reinterpret_cast<uint2*>(y + nb) = make_uint2(pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7]));
+    }
+};
+
+// The tokens [t0, t0 + ntok) of a CTA's `nout` outputs from n0, by 256 threads; partial sums at `part`
+// (fp32 [slice][rows][128], slices `rows` tokens apart).
+template <bool F8, bool GATED, int SPLIT>
+__device__ __forceinline__ void linear_join(const LinearParams& p, const float* part, int rows, long long t0,
+                                            int ntok, int n0, int nout, int tid) {
+    const int stride = rows * LIN_BM;
+    if ((p.N & 3) == 0) {
+        LinearCols<F8, GATED> c;
+        c.load(p, tid, n0, nout);
+#pragma unroll 2
+        for (int tok = tid >> 4; tok < ntok; tok += 16) {
+            uint2 ra, rb;
+            c.residual(p, t0 + tok, ra, rb);
+            c.template finish<SPLIT>(p, part + tok * LIN_BM, stride, t0 + tok, ra, rb);
+        }
+    } else {
+        // rows of y start at any 2-byte address: an output per thread
+        constexpr int FT = GATED ? 64 : 128;
+        constexpr int STEP = 256 / FT;
+        const int f = tid % FT, n = n0 + f;
+        if (f >= nout) return;
+        const float ba = p.bias ? __ldg(p.bias + n) : 0.0f, bb = GATED && p.bias_up ? __ldg(p.bias_up + n) : 0.0f;
+        const float wa = F8 ? __ldg(p.sw + n) : 1.0f, wb = F8 && GATED ? __ldg(p.sw_up + n) : 1.0f;
+#pragma unroll 4
+        for (int tok = tid / FT; tok < ntok; tok += STEP) {
+            const long long o = (t0 + tok) * p.N + n;
+            const float res = p.residual ? __bfloat162float(p.residual[o]) : 0.0f;
+            const float sx = F8 ? __ldg(p.sx + t0 + tok) : 1.0f;
+            float a = part[tok * LIN_BM + f], b = GATED ? part[tok * LIN_BM + 64 + f] : 0.0f;
+#pragma unroll
+            for (int r = 1; r < SPLIT; ++r) {
+                a += part[r * stride + tok * LIN_BM + f];
+                if (GATED) b += part[r * stride + tok * LIN_BM + 64 + f];
+            }
+            if (F8) { a *= sx * wa; b *= sx * wb; }
+            a += ba;
+            a = GATED ? swiglu_f32(a, b + bb) : linear_act(p.act, a);
+            p.y[o] = __float2bfloat16_rn(p.residual ? a + res : a);
+        }
+    }
+}
+
+// tcgen05 shapes: M = 128 CG, N = bn; tensor maps: W / W_up with boxes of 128 rows (SwiGLU: 64), x with
+// boxes of bn / CG rows.  grid = tiles * split * CG, cluster = the split * CG CTAs of one tile.
+template <bool F8, bool GATED, int CG>
 __global__ void __launch_bounds__(LIN_THREADS)
 linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWup,
                     const __grid_constant__ CUtensorMap tmX, const __grid_constant__ LinearParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int S = p.stages, x_bytes = p.bn * 128;
+    const int S = p.stages, x_rows = p.bn / CG, x_bytes = x_rows * 128;
     uint8_t* sW = smem;
     uint8_t* sX = smem + S * LIN_A_BYTES;
-    uint64_t* full_bar = reinterpret_cast<uint64_t*>(sX + S * x_bytes);
+    // partial sums: over the ring, or (small tiles) in shared memory of their own, where another rank may
+    // write them while this one's ring is still in use
+    float* part = reinterpret_cast<float*>(p.own_part ? sX + S * x_bytes : smem);
+    uint64_t* full_bar = reinterpret_cast<uint64_t*>(sX + S * x_bytes + (p.own_part ? linear_part_bytes(p.bn, p.split) : 0));
     uint64_t* empty_bar = full_bar + S;
     uint64_t* done_bar = empty_bar + S;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tile = blockIdx.x / p.split, rank = blockIdx.x - tile * p.split;
+    const int csize = p.split * CG;
+    const int tile = blockIdx.x / csize, rank = blockIdx.x - tile * csize;   // = the rank in the cluster
+    const int slice = rank / CG, cta = rank - slice * CG;                    // K slice; CTA of its pair
+    const bool leader = cta == 0;
     const int m_idx = tile % p.mt, n_idx = tile / p.mt;
-    constexpr int FT = GATED ? 64 : 128;           // outputs per tile
-    const int n0 = n_idx * FT;
+    constexpr int FT = GATED ? 64 : 128;           // outputs per CTA
+    const int n0 = (n_idx * CG + cta) * FT;
     const int t0 = m_idx * p.bn;                   // first token
     const int ntok = min(p.bn, p.M - t0);
     constexpr int KB = F8 ? 128 : 64;              // K elements per 128-byte stage row
     const int nk = (p.K + KB - 1) / KB;
-    const int kb0 = (int)((long long)nk * rank / p.split), kb1 = (int)((long long)nk * (rank + 1) / p.split);
+    const int kb0 = (int)((long long)nk * slice / p.split), kb1 = (int)((long long)nk * (slice + 1) / p.split);
+    const int nout = min(FT, p.N - n0);            // <= 0: a pair's second CTA past the last output
+    const int own = (ntok + p.split - 1) / p.split;               // tokens joined by each slice's rank
+    const int my_t0 = min(slice * own, ntok), my_ntok = min(own, ntok - my_t0);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -118,40 +272,60 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
         if (GATED) prefetch_tensormap(&tmWup);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, p.tmem_cols);
-        tmem_relinquish();
+        if (CG == 2) {
+            tmem_alloc_pair(tmem_slot, p.tmem_cols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, p.tmem_cols);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
+    // every CTA of the cluster runs, and a pair's barriers are initialised, before remote accesses
+    if (CG == 2) cluster_sync_all();
+    else if (p.split > 1) cluster_arrive();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    grid_wait();
+    grid_launch_next();
 
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t pol_w = p.mt == 1 ? policy_evict_first() : policy_evict_normal();
             const uint64_t pol_x = policy_evict_last();
-            const uint32_t bytes = LIN_A_BYTES + (uint32_t)x_bytes;
+            const uint32_t bytes = CG * (LIN_A_BYTES + (uint32_t)x_bytes);   // of both CTAs of a pair
+            const uint32_t full_leader = map_to_cta(full_bar, (uint32_t)(rank - cta));
             int issued = 0;
             bool ok = true;
             for (int kb = kb0; kb < kb1; ++kb) {
                 const int s = issued % S;
                 if (!mbar_wait(empty_bar + s, ((issued / S) & 1) ^ 1u, abort_flag)) { ok = false; break; }
-                mbar_arrive_expect_tx(full_bar + s, bytes);
+                if (leader) mbar_arrive_expect_tx(full_bar + s, bytes);
                 uint8_t* w_dst = sW + s * LIN_A_BYTES;
-                tma_load_2d(w_dst, &tmW, full_bar + s, kb * KB, n0, pol_w);
-                if (GATED) tma_load_2d(w_dst + 64 * 128, &tmWup, full_bar + s, kb * KB, n0, pol_w);
-                tma_load_2d(sX + s * x_bytes, &tmX, full_bar + s, kb * KB, t0, pol_x);
+                const int tx = t0 + cta * x_rows;
+                if (CG == 2) {
+                    const uint32_t fb = full_leader + (uint32_t)s * 8u;
+                    tma_load_2d_pair(w_dst, &tmW, fb, kb * KB, n0, pol_w);
+                    if (GATED) tma_load_2d_pair(w_dst + 64 * 128, &tmWup, fb, kb * KB, n0, pol_w);
+                    tma_load_2d_pair(sX + s * x_bytes, &tmX, fb, kb * KB, tx, pol_x);
+                } else {
+                    tma_load_2d(w_dst, &tmW, full_bar + s, kb * KB, n0, pol_w);
+                    if (GATED) tma_load_2d(w_dst + 64 * 128, &tmWup, full_bar + s, kb * KB, n0, pol_w);
+                    tma_load_2d(sX + s * x_bytes, &tmX, full_bar + s, kb * KB, tx, pol_x);
+                }
                 ++issued;
             }
-            if (!ok) {
+            if (!ok && leader) {
                 const int n = issued < S ? issued : S;      // copies in flight land before exit
                 for (int i = 1; i <= n; ++i)
                     mbar_wait(full_bar + ((issued - i) % S), (uint32_t)(((issued - i) / S) & 1), nullptr);
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = F8 ? idesc_e4m3_f32(LIN_BM, p.bn) : idesc_bf16_f32(LIN_BM, p.bn);
+        if (lane == 0 && leader) {
+            const uint32_t idesc = F8 ? idesc_e4m3_f32(LIN_BM * CG, p.bn) : idesc_bf16_f32(LIN_BM * CG, p.bn);
+            const uint16_t both = (uint16_t)(3u << rank);    // this CTA and its peer
             for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
                 const int s = i % S;
                 if (!mbar_wait(full_bar + s, (i / S) & 1, abort_flag)) break;
@@ -160,123 +334,318 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
                 const uint64_t bd = smem_desc_k_sw128(sX + s * x_bytes);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                    if (F8) umma_e4m3(tmem_base, ad + 2ull * kk, bd + 2ull * kk, idesc, (i | kk) != 0);
-                    else umma_bf16(tmem_base, ad + 2ull * kk, bd + 2ull * kk, idesc, (i | kk) != 0);
-                }
-                umma_commit(empty_bar + s);
-            }
-            umma_commit(done_bar);       // all MMAs retired: the accumulator is final, the ring is idle
-            mbar_wait(done_bar, 0, nullptr);
-        }
-    } else {
-        const bool ready = mbar_wait(done_bar, 0, nullptr);
-        if (__all_sync(0xffffffffu, ready)) {
-            tc_fence_after();
-            const int sub = warp & 3;
-            float* stage = reinterpret_cast<float*>(smem);
-            const uint32_t tbase = tmem_base + ((uint32_t)(sub * 32) << 16);
-            for (int c = 0; c < ntok; c += 32) {            // tmem_cols is a multiple of 32
-                uint32_t v[32];
-                __syncwarp();
-                tmem_ld_32cols(tbase + c, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (c + j < ntok) stage[(c + j) * LIN_BM + sub * 32 + lane] = __uint_as_float(v[j]);
-            }
-            tc_fence_before();
-        }
-    }
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem_base, p.tmem_cols);
-    }
-    if (p.split > 1) cluster_sync_all();                     // every rank's partial sums are staged
-
-    // ---- join the ranks' sums, epilogue, store: rank r takes an equal share of the tile's units
-    const uint32_t stage0 = smem_u32(smem);
-    auto peer = [&](int r) {
-        uint32_t a;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(stage0), "r"(r));
-        return a;
-    };
-    const int nout = min(FT, p.N - n0);
-    if ((p.N & 7) == 0) {
-        const int per_tok = nout >> 3;                       // units of 8 outputs of a token
-        const int units = ntok * per_tok;
-        const int u0 = (int)((long long)units * rank / p.split), u1 = (int)((long long)units * (rank + 1) / p.split);
-        for (int u = u0 + threadIdx.x; u < u1; u += LIN_THREADS) {
-            const int tok = u / per_tok, f = (u - tok * per_tok) * 8;
-            const long long row = t0 + tok;
-            float z[8], up[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = up[i] = 0.0f;
-            for (int r = 0; r < p.split; ++r) {
-                const uint32_t a = peer(r) + (uint32_t)(tok * LIN_BM + f) * 4u;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float4 v = ld_cluster_f4(a + 16 * h);
-                    z[4 * h] += v.x; z[4 * h + 1] += v.y; z[4 * h + 2] += v.z; z[4 * h + 3] += v.w;
-                    if (GATED) {
-                        const float4 q = ld_cluster_f4(a + 256 + 16 * h);
-                        up[4 * h] += q.x; up[4 * h + 1] += q.y; up[4 * h + 2] += q.z; up[4 * h + 3] += q.w;
+                    if (CG == 2) {
+                        if (F8) umma_e4m3_pair(tmem_base, ad + 2ull * kk, bd + 2ull * kk, idesc, (i | kk) != 0);
+                        else umma_bf16_pair(tmem_base, ad + 2ull * kk, bd + 2ull * kk, idesc, (i | kk) != 0);
+                    } else {
+                        if (F8) umma_e4m3(tmem_base, ad + 2ull * kk, bd + 2ull * kk, idesc, (i | kk) != 0);
+                        else umma_bf16(tmem_base, ad + 2ull * kk, bd + 2ull * kk, idesc, (i | kk) != 0);
                     }
                 }
+                if (CG == 2) umma_commit_pair(empty_bar + s, both);
+                else umma_commit(empty_bar + s);
             }
-            const int n = n0 + f;
-            const float sx = F8 ? __ldg(p.sx + row) : 1.0f;
-            float res[8];
-            if (p.residual) bf16x8_to_f32(*reinterpret_cast<const uint4*>(p.residual + row * p.N + n), res);
-            float o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float a = z[i];
-                if (F8) a *= sx * __ldg(p.sw + n + i);
-                if (p.bias) a += __ldg(p.bias + n + i);
-                if (GATED) {
-                    float b = up[i];
-                    if (F8) b *= sx * __ldg(p.sw_up + n + i);
-                    if (p.bias_up) b += __ldg(p.bias_up + n + i);
-                    a = swiglu_f32(a, b);
-                } else {
-                    a = linear_act(p.act, a);
-                }
-                o[i] = p.residual ? a + res[i] : a;
-            }
-            *reinterpret_cast<uint4*>(p.y + row * p.N + n) =
-                make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                           pack_bf16x2(o[6], o[7]));
+            // all MMAs retired: the accumulator is final, the ring is idle
+            if (CG == 2) umma_commit_pair(done_bar, both);
+            else umma_commit(done_bar);
+            mbar_wait(done_bar, 0, nullptr);
         }
-    } else {
-        const int units = ntok * nout;                       // output rows start at any 2-byte address
-        const int u0 = (int)((long long)units * rank / p.split), u1 = (int)((long long)units * (rank + 1) / p.split);
-        for (int u = u0 + threadIdx.x; u < u1; u += LIN_THREADS) {
-            const int tok = u / nout, f = u - tok * nout;
-            const long long row = t0 + tok;
-            const int n = n0 + f;
-            float a = 0.0f, b = 0.0f;
-            for (int r = 0; r < p.split; ++r) {
-                const uint32_t q = peer(r) + (uint32_t)(tok * LIN_BM + f) * 4u;
-                a += ld_cluster_f1(q);
-                if (GATED) b += ld_cluster_f1(q + 256);
+    } else if (warp < 4) {
+        const int tid = threadIdx.x - 64;
+        if (p.residual && nout > 0) {                            // a row's segment is at most 3 lines of 128 bytes
+            for (int i = tid; i < my_ntok * 3; i += 64) {
+                const int tok = i / 3, col = min((i - tok * 3) * 64, nout - 1);
+                prefetch_l2(p.residual + (long long)(t0 + my_t0 + tok) * p.N + n0 + col);
             }
-            const float sx = F8 ? __ldg(p.sx + row) : 1.0f;
-            if (F8) a *= sx * __ldg(p.sw + n);
-            if (p.bias) a += __ldg(p.bias + n);
-            if (GATED) {
-                if (F8) b *= sx * __ldg(p.sw_up + n);
-                if (p.bias_up) b += __ldg(p.bias_up + n);
-                a = swiglu_f32(a, b);
-            } else {
-                a = linear_act(p.act, a);
-            }
-            if (p.residual) a += __bfloat162float(p.residual[row * p.N + n]);
-            p.y[row * p.N + n] = __float2bfloat16_rn(a);
+        }
+        if (tid * 32 < nout) {
+            if (p.bias) prefetch_l2(p.bias + n0 + tid * 32);
+            if (GATED && p.bias_up) prefetch_l2(p.bias_up + n0 + tid * 32);
+            if (F8) prefetch_l2(p.sw + n0 + tid * 32);
+            if (F8 && GATED) prefetch_l2(p.sw_up + n0 + tid * 32);
         }
     }
     __syncwarp();
-    if (p.split > 1) cluster_sync_all();                     // no peer reads this CTA's shared memory any more
+    if (CG == 1 && p.split > 1) cluster_wait();                  // the arrival at the start
+    const bool ready = __all_sync(0xffffffffu, mbar_wait(done_bar, 0, nullptr));
+    if (p.split > 1 && !p.own_part) cluster_sync_all();          // every rank's ring is idle
+    if (ready) {
+        tc_fence_after();
+        const int sub = warp & 3;
+        const uint32_t tbase = tmem_base + ((uint32_t)(sub * 32) << 16);
+        const uint32_t part0 = smem_u32(part) + (uint32_t)(sub * 32 + lane) * 4u;
+        for (int c = (warp >> 2) * 32; c < ntok; c += 64) {      // tmem_cols is a multiple of 32
+            uint32_t v[32];
+            __syncwarp();
+            tmem_ld_32cols(tbase + c, v);
+            tmem_ld_wait();
+            if (p.split == 1) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (c + j < ntok) part[(c + j) * LIN_BM + sub * 32 + lane] = __uint_as_float(v[j]);
+            } else {
+                int q = c / own, in_q = c - q * own;             // the owner of column c, and its place there
+                uint32_t at = map_to_cta_addr(part0, (uint32_t)(cta + CG * q)) + (uint32_t)(slice * own) * (LIN_BM * 4);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    if (c + j < ntok) st_cluster_f1(at + (uint32_t)in_q * (LIN_BM * 4), __uint_as_float(v[j]));
+                    if (++in_q == own) {
+                        in_q = 0;
+                        ++q;
+                        if (c + j + 1 < ntok)
+                            at = map_to_cta_addr(part0, (uint32_t)(cta + CG * q)) + (uint32_t)(slice * own) * (LIN_BM * 4);
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    if (CG * p.split > 1) cluster_sync_all();                    // all partial sums have arrived
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        if (CG == 2) tmem_dealloc_pair(tmem_base, p.tmem_cols);
+        else tmem_dealloc(tmem_base, p.tmem_cols);
+    }
+    if (nout <= 0 || my_ntok <= 0) return;
+    const long long first = t0 + my_t0;
+    if (p.split == 1) linear_join<F8, GATED, 1>(p, part, own, first, my_ntok, n0, nout, threadIdx.x);
+    else if (p.split == 2) linear_join<F8, GATED, 2>(p, part, own, first, my_ntok, n0, nout, threadIdx.x);
+    else if (p.split == 4) linear_join<F8, GATED, 4>(p, part, own, first, my_ntok, n0, nout, threadIdx.x);
+    else linear_join<F8, GATED, 8>(p, part, own, first, my_ntok, n0, nout, threadIdx.x);
+}
+
+// ---------------------------------------------------------------- many tokens: persistent CTA pairs
+//
+// Tiles of 256 weight rows x up to 256 tokens by CTA pairs (cta_group::2: each CTA holds 128 weight rows
+// and half of the tokens: 32 KB of operands per 64 K-elements for 256 x 128 outputs per SM), a 6-stage
+// ring and two accumulators, so that a tile's epilogue runs under the next tile's products.  The eight
+// epilogue warps move 32 tokens of the accumulator at a time to shared memory (double buffered), then
+// each thread finishes its outputs of two tokens, the residual of the next 32 already on its way.
+// The last token tile runs its MMAs with N = its tokens rounded up to 16.
+constexpr int LINP_STAGES = 6;
+constexpr int LINP_STAGE_BYTES = LIN_A_BYTES + 128 * 128;          // 128 weight rows + 128 tokens
+constexpr int LINP_CHUNK = 32;                                     // tokens per epilogue step
+constexpr int LINP_CHUNK_BYTES = LINP_CHUNK * LIN_BM * 4;
+constexpr int LINP_THREADS = 320;                                  // TMA, MMA, 8 epilogue warps
+constexpr int LINP_SMEM_BYTES = LINP_STAGES * LINP_STAGE_BYTES + 2 * LINP_CHUNK_BYTES + 1024 + 256;
+// Token tiles walked together: 16 tiles of 256 tokens at K = 4096 are 33 MB, which stay in L2 while the
+// weights pass by once; all token tiles of M = 16384 would not.
+constexpr int LINP_GROUP = 16;
+
+struct LinearTile {
+    int t0, ntok, n_idx;
+};
+
+__device__ __forceinline__ LinearTile linear_tile(const LinearParams& p, int t, int nt) {
+    const int per = LINP_GROUP * nt, g = t / per, m0 = g * LINP_GROUP;
+    const int gm = min(LINP_GROUP, p.mt - m0), in = t - g * per;
+    LinearTile r;
+    r.n_idx = in / gm;
+    r.t0 = (m0 + in - r.n_idx * gm) * p.bn;
+    r.ntok = min(p.bn, p.M - r.t0);
+    return r;
+}
+
+__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+
+// Tensor maps as for linear_split_kernel with CG = 2; bn = 256.
+template <bool F8, bool GATED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LINP_THREADS, 1)
+linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWup,
+                   const __grid_constant__ CUtensorMap tmX, const __grid_constant__ LinearParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sW = smem;
+    uint8_t* sX = smem + LINP_STAGES * LIN_A_BYTES;
+    float* chunk = reinterpret_cast<float*>(smem + LINP_STAGES * LINP_STAGE_BYTES);
+    uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + LINP_STAGES * LINP_STAGE_BYTES + 2 * LINP_CHUNK_BYTES);
+    uint64_t* empty_bar = full_bar + LINP_STAGES;
+    uint64_t* tfull_bar = empty_bar + LINP_STAGES;
+    uint64_t* tempty_bar = tfull_bar + 2;
+    uint64_t* drain_bar = tempty_bar + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    constexpr int FT = GATED ? 64 : 128;           // outputs per CTA
+    constexpr int KB = F8 ? 128 : 64;
+    const int nk = (p.K + KB - 1) / KB;
+    const int nt = (p.N + 2 * FT - 1) / (2 * FT);
+    const int total = nt * p.mt;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < LINP_STAGES; ++s) {
+            mbar_init(full_bar + s, 1);
+            mbar_init(empty_bar + s, 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull_bar + a, 1);
+            mbar_init(tempty_bar + a, 16);         // the epilogue warps of both CTAs
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmX);
+        if (GATED) prefetch_tensormap(&tmWup);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, GEMM_TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    grid_wait();
+    grid_launch_next();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol_w = policy_evict_normal(), pol_x = policy_evict_last();
+            const uint32_t full_leader = map_to_cta(full_bar, 0);
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = pair; t < total && ok; t += npairs) {
+                const LinearTile ti = linear_tile(p, t, nt);
+                const int n0 = (ti.n_idx * 2 + rank) * FT;
+                const int half = ((ti.ntok + 15) & ~15) >> 1;       // tokens per CTA of this tile
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!mbar_wait(empty_bar + stage, phase ^ 1u, abort_flag)) { ok = false; break; }
+                    const uint32_t fb = full_leader + (uint32_t)stage * 8u;
+                    if (leader) mbar_arrive_expect_tx(full_bar + stage, 2u * LINP_STAGE_BYTES);
+                    uint8_t* w_dst = sW + stage * LIN_A_BYTES;
+                    tma_load_2d_pair(w_dst, &tmW, fb, kb * KB, n0, pol_w);
+                    if (GATED) tma_load_2d_pair(w_dst + 64 * 128, &tmWup, fb, kb * KB, n0, pol_w);
+                    tma_load_2d_pair(sX + stage * 128 * 128, &tmX, fb, kb * KB, ti.t0 + rank * half, pol_x);
+                    ++issued;
+                    if (++stage == LINP_STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if (!ok && leader) {
+                const int n = issued < LINP_STAGES ? issued : LINP_STAGES;
+                for (int i = 1; i <= n; ++i) {
+                    const int q = issued - i;
+                    mbar_wait(full_bar + (q % LINP_STAGES), (uint32_t)((q / LINP_STAGES) & 1), nullptr);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool any = false, ok = true;
+            for (int t = pair; t < total && ok; t += npairs) {
+                const LinearTile ti = linear_tile(p, t, nt);
+                const int n = (ti.ntok + 15) & ~15;
+                const uint32_t idesc = F8 ? idesc_e4m3_f32(256, n) : idesc_bf16_f32(256, n);
+                if (!mbar_wait(tempty_bar + acc, acc_phase ^ 1u, abort_flag)) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + (uint32_t)(acc * GEMM_ACC_COLS);
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!mbar_wait(full_bar + stage, phase, abort_flag)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint64_t ad = smem_desc_k_sw128(sW + stage * LIN_A_BYTES);
+                    const uint64_t bd = smem_desc_k_sw128(sX + stage * 128 * 128);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (F8) umma_e4m3_pair(d, ad + 2ull * kk, bd + 2ull * kk, idesc, (kb | kk) != 0);
+                        else umma_bf16_pair(d, ad + 2ull * kk, bd + 2ull * kk, idesc, (kb | kk) != 0);
+                    }
+                    umma_commit_pair(empty_bar + stage, 0x3);
+                    any = true;
+                    if (++stage == LINP_STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                umma_commit_pair(tfull_bar + acc, 0x3);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            if (any) {
+                umma_commit_pair(drain_bar, 0x1);
+                mbar_wait(drain_bar, 0, nullptr);
+            }
+        }
+    } else {
+        const int sub = warp & 3, half = (warp - 2) >> 2;           // lane quarter; half of a chunk's columns
+        const int tid = threadIdx.x - 64;
+        const uint32_t tempty_leader = map_to_cta(tempty_bar, 0);
+        int acc = 0, buf = 0;
+        uint32_t acc_phase = 0;
+        const bool vec = (p.N & 3) == 0;
+        for (int t = pair; t < total; t += npairs) {
+            const LinearTile ti = linear_tile(p, t, nt);
+            const int n0 = (ti.n_idx * 2 + rank) * FT, nout = min(FT, p.N - n0);
+            LinearCols<F8, GATED> cols;
+            uint2 ra[2], rb[2];
+            const int tk = tid >> 4;
+            if (vec) {
+                cols.load(p, tid, n0, nout);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    cols.residual(p, ti.t0 + min(tk + 16 * i, ti.ntok - 1), ra[i], rb[i]);
+            }
+            const bool ready = mbar_wait(tfull_bar + acc, acc_phase, abort_flag);
+            __syncwarp();
+            if (!named_barrier_all(1, 256, ready)) break;           // all eight warps go on, or none
+            tc_fence_after();
+            const uint32_t tbase = tmem_base + (uint32_t)(acc * GEMM_ACC_COLS) + ((uint32_t)(sub * 32) << 16) + half * 16;
+            for (int c = 0; c < ti.ntok; c += LINP_CHUNK) {
+                uint32_t v[16];
+                __syncwarp();
+                tmem_ld_16cols(tbase + c, v);
+                tmem_ld_wait();
+                float* dst = chunk + buf * (LINP_CHUNK * LIN_BM);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) dst[(half * 16 + j) * LIN_BM + sub * 32 + lane] = __uint_as_float(v[j]);
+                if (c + LINP_CHUNK >= ti.ntok) {                    // the accumulator has been read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + (uint32_t)acc * 8u);
+                }
+                named_barrier(1, 256);                              // the chunk is staged
+                if (vec) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int tok = c + tk + 16 * i;
+                        const uint2 xa = ra[i], xb = rb[i];
+                        if (c + LINP_CHUNK < ti.ntok)
+                            cols.residual(p, ti.t0 + min(tok + LINP_CHUNK, ti.ntok - 1), ra[i], rb[i]);
+                        if (tok < ti.ntok)
+                            cols.template finish<1>(p, dst + (tk + 16 * i) * LIN_BM, 0, ti.t0 + tok, xa, xb);
+                    }
+                } else {
+                    linear_join<F8, GATED, 1>(p, dst, LINP_CHUNK, ti.t0 + c, min(LINP_CHUNK, ti.ntok - c), n0, nout, tid);
+                }
+                buf ^= 1;
+            }
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+    }
+
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, GEMM_TMEM_COLS);
+    }
 }
 
 }  // namespace moe

@@ -1256,8 +1256,27 @@ int check_linear(const void* x, const void* W, const void* W_up, const float* s,
     return MOE_OK;
 }
 
-template <bool F8, bool GATED>
-int launch_linear_split(const LinearArgs& a, cudaStream_t s) {
+// Launch attributes of the dense layer's and the scored router's kernels: cluster size and programmatic
+// stream serialization (their prologue overlaps the end of the kernel in front of them; see grid_wait()).
+struct LaunchAttrs {
+    cudaLaunchAttribute a[2];
+    LaunchAttrs(cudaLaunchConfig_t* cfg, unsigned grid, unsigned block, size_t smem, cudaStream_t s, int cluster) {
+        memset(cfg, 0, sizeof(*cfg));
+        cfg->gridDim = dim3(grid);
+        cfg->blockDim = dim3(block);
+        cfg->dynamicSmemBytes = smem;
+        cfg->stream = s;
+        a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        a[0].val.programmaticStreamSerializationAllowed = 1;
+        a[1].id = cudaLaunchAttributeClusterDimension;
+        a[1].val.clusterDim.x = cluster;
+        a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;
+        cfg->attrs = a;
+        cfg->numAttrs = cluster > 1 ? 2 : 1;
+    }
+};
+
+LinearParams linear_params(const LinearArgs& a) {
     LinearParams p;
     memset(&p, 0, sizeof(p));
     p.M = a.M; p.N = a.N; p.K = a.K; p.act = a.act;
@@ -1265,65 +1284,105 @@ int launch_linear_split(const LinearArgs& a, cudaStream_t s) {
     p.residual = reinterpret_cast<const __nv_bfloat16*>(a.residual);
     p.y = reinterpret_cast<__nv_bfloat16*>(a.y);
     p.sx = a.sx; p.sw = a.sw; p.sw_up = a.sw_up;
+    return p;
+}
+
+// Weights in boxes of 128 rows (GATED: 64 of each), x in boxes of x_rows.
+template <bool F8, bool GATED>
+int linear_maps(const LinearArgs& a, int x_rows, CUtensorMap* mW, CUtensorMap* mWup, CUtensorMap* mX) {
+    auto mk = [&](CUtensorMap* m, const void* base, uint64_t rows, uint32_t box) {
+        return F8 ? make_map_e4m3(m, base, a.K, rows, box) : make_map(m, base, a.K, rows, box);
+    };
+    int rc;
+    if ((rc = mk(mW, a.W, a.N, GATED ? 64 : 128)) != MOE_OK) return rc;
+    if (GATED) {
+        if ((rc = mk(mWup, a.W_up, a.N, 64)) != MOE_OK) return rc;
+    } else {
+        *mWup = *mW;
+    }
+    return mk(mX, a.x, a.M, x_rows);
+}
+
+// Lets a kernel use the whole opt-in shared memory on this device (once per kernel and device).
+template <auto Kernel>
+int linear_smem_attr() {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    static bool attr_set[kMaxDevices] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!attr_set[dev]) {
+        if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM_MAX) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        attr_set[dev] = true;
+    }
+    return MOE_OK;
+}
+
+template <bool F8, bool GATED, int CG>
+int launch_linear_split(const LinearArgs& a, cudaStream_t s) {
+    LinearParams p = linear_params(a);
     // token tiles of equal size (multiples of 16)
     const int mt0 = (a.M + 255) / 256;
     p.bn = ((a.M + mt0 - 1) / mt0 + 15) / 16 * 16;
     p.mt = (a.M + p.bn - 1) / p.bn;
     p.tmem_cols = p.bn <= 32 ? 32 : p.bn <= 64 ? 64 : p.bn <= 128 ? 128 : 256;
-    const int nt = (a.N + (GATED ? 63 : 127)) / (GATED ? 64 : 128);
+    constexpr int FT = (GATED ? 64 : 128) * CG;
+    const int nt = (a.N + FT - 1) / FT;
     const int nk = (a.K + (F8 ? 127 : 63)) / (F8 ? 128 : 64);
     p.stages = 4;
     p.split = 1;
+    p.own_part = p.split > 1 && p.bn <= 32;
+    while (!p.own_part && p.stages * (LIN_A_BYTES + p.bn / CG * 128) < linear_part_bytes(p.bn, p.split)) ++p.stages;
     const long long tiles = (long long)nt * p.mt;
-    if (tiles * p.split >= (1ll << 31)) return MOE_ERR_SHAPE;
+    if (tiles * p.split * CG >= (1ll << 31)) return MOE_ERR_SHAPE;
     (void)nk;
     CUtensorMap mW, mWup, mX;
-    auto mk = [&](CUtensorMap* m, const void* base, uint64_t rows, uint32_t box) {
-        return F8 ? make_map_e4m3(m, base, a.K, rows, box) : make_map(m, base, a.K, rows, box);
-    };
-    int rc;
-    if ((rc = mk(&mW, a.W, a.N, GATED ? 64 : 128)) != MOE_OK) return rc;
-    if (GATED) {
-        if ((rc = mk(&mWup, a.W_up, a.N, 64)) != MOE_OK) return rc;
-    } else {
-        mWup = mW;
-    }
-    if ((rc = mk(&mX, a.x, a.M, p.bn)) != MOE_OK) return rc;
-    {
-        std::lock_guard<std::mutex> lock(g_mutex);
-        static bool attr_set[kMaxDevices] = {};
-        int dev = 0;
-        cudaGetDevice(&dev);
-        if (!attr_set[dev]) {
-            if (cudaFuncSetAttribute(linear_split_kernel<F8, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     GEMM_SMEM_MAX) != cudaSuccess)
-                return MOE_ERR_CUDA;
-            attr_set[dev] = true;
-        }
-    }
+    int rc = linear_maps<F8, GATED>(a, p.bn / CG, &mW, &mWup, &mX);
+    if (rc != MOE_OK) return rc;
+    if ((rc = linear_smem_attr<linear_split_kernel<F8, GATED, CG>>()) != MOE_OK) return rc;
     cudaLaunchConfig_t cfg;
-    memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)(tiles * p.split));
-    cfg.blockDim = dim3(LIN_THREADS);
-    cfg.dynamicSmemBytes = linear_smem_bytes(p.stages, p.bn);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.split;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, linear_split_kernel<F8, GATED>, mW, mWup, mX, p) != cudaSuccess) {
+    const LaunchAttrs attrs(&cfg, (unsigned)(tiles * p.split * CG), LIN_THREADS,
+                            linear_smem_bytes(p.stages, p.bn / CG, p.own_part ? linear_part_bytes(p.bn, p.split) : 0), s, p.split * CG);
+    if (cudaLaunchKernelEx(&cfg, linear_split_kernel<F8, GATED, CG>, mW, mWup, mX, p) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
     return MOE_OK;
 }
 
+template <bool F8, bool GATED>
+int launch_linear_pair(DeviceInfo* di, const LinearArgs& a, cudaStream_t s) {
+    LinearParams p = linear_params(a);
+    p.bn = 256;
+    p.mt = (a.M + 255) / 256;
+    const int nt = (a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
+    const long long tiles = (long long)nt * p.mt;
+    if (tiles >= (1ll << 30)) return MOE_ERR_SHAPE;
+    CUtensorMap mW, mWup, mX;
+    int rc = linear_maps<F8, GATED>(a, 128, &mW, &mWup, &mX);
+    if (rc != MOE_OK) return rc;
+    if ((rc = linear_smem_attr<linear_pair_kernel<F8, GATED>>()) != MOE_OK) return rc;
+    const long long pairs = di->sms / 2;
+    cudaLaunchConfig_t cfg;
+    const LaunchAttrs attrs(&cfg, 2 * (unsigned)std::min(tiles, pairs), LINP_THREADS, LINP_SMEM_BYTES, s, 1);
+    if (cudaLaunchKernelEx(&cfg, linear_pair_kernel<F8, GATED>, mW, mWup, mX, p) != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
+}
+
+template <bool F8, bool GATED>
+int run_linear_as(DeviceInfo* di, const LinearArgs& a, cudaStream_t s) {
+    const int kind = a.M > 1024 ? 3 : 1;
+    return kind == 3   ? launch_linear_pair<F8, GATED>(di, a, s)
+           : kind == 2 ? launch_linear_split<F8, GATED, 2>(a, s)
+                       : launch_linear_split<F8, GATED, 1>(a, s);
+}
+
 template <bool F8>
-int run_linear(const LinearArgs& a, cudaStream_t s) {
-    return a.act == MOE_ACT_SWIGLU ? launch_linear_split<F8, true>(a, s) : launch_linear_split<F8, false>(a, s);
+int run_linear(DeviceInfo* di, const LinearArgs& a, cudaStream_t s) {
+    return a.act == MOE_ACT_SWIGLU ? run_linear_as<F8, true>(di, a, s) : run_linear_as<F8, false>(di, a, s);
 }
 
 size_t linear_scale_offset(int M, int K) { return align256((size_t)M * K); }
@@ -1340,7 +1399,7 @@ int moe_linear(const moe_bf16* x, const moe_bf16* W, const moe_bf16* W_up, const
     DeviceInfo* di;
     if ((rc = device_info(&di)) != MOE_OK) return rc;
     const LinearArgs a = {x, W, W_up, nullptr, nullptr, nullptr, bias, bias_up, residual, M, N, K, act, y};
-    return run_linear<false>(a, static_cast<cudaStream_t>(stream));
+    return run_linear<false>(di, a, static_cast<cudaStream_t>(stream));
 }
 
 int moe_linear_workspace_bytes(int M, int K, size_t* bytes) {
@@ -1367,7 +1426,7 @@ int moe_linear_w8a8(const moe_bf16* x, const uint8_t* Wq, const float* s, const 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((rc = run_quant_h(x, nullptr, M, K, xq, sx, st)) != MOE_OK) return rc;
     const LinearArgs a = {xq, Wq, Wq_up, sx, s, s_up, bias, bias_up, residual, M, N, K, act, y};
-    return run_linear<true>(a, st);
+    return run_linear<true>(di, a, st);
 }
 
 int moe_layer_forward_ex(const moe_bf16* x, const moe_bf16* Wg, const float* bias, const moe_bf16* W1,
