@@ -71,24 +71,25 @@ __device__ __forceinline__ void st_cluster_f1(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// act of eight values; the branch on act is taken once
-__device__ __forceinline__ void linear_act8(int act, float (&z)[8]) {
+// act of C values; the branch on act is taken once
+template <int C>
+__device__ __forceinline__ void linear_acts(int act, float (&z)[C]) {
     switch (act) {
         case LIN_RELU:
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = linear_act(LIN_RELU, z[i]);
+            for (int i = 0; i < C; ++i) z[i] = linear_act(LIN_RELU, z[i]);
             break;
         case LIN_SILU:
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = linear_act(LIN_SILU, z[i]);
+            for (int i = 0; i < C; ++i) z[i] = linear_act(LIN_SILU, z[i]);
             break;
         case LIN_GELU:
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = linear_act(LIN_GELU, z[i]);
+            for (int i = 0; i < C; ++i) z[i] = linear_act(LIN_GELU, z[i]);
             break;
         case LIN_GELU_TANH:
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = linear_act(LIN_GELU_TANH, z[i]);
+            for (int i = 0; i < C; ++i) z[i] = linear_act(LIN_GELU_TANH, z[i]);
             break;
         default: break;
     }
@@ -162,7 +163,7 @@ struct LinearCols {
 #pragma unroll
             for (int i = 0; i < 4; ++i) z[i] = swiglu_f32(z[i], z[i + 4]);
         } else {
-            linear_act8(p.act, z);
+            linear_acts(p.act, z);
         }
         if (p.residual) {
             float res[8];
@@ -416,6 +417,128 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     else linear_join<F8, GATED, 8>(p, part, own, first, my_ntok, n0, nout, threadIdx.x);
 }
 
+// ---------------------------------------------------------------- up to four tokens: a warp per weight rows
+//
+// A stream of weights with a few multiply-adds per element: four weight rows per warp (GATED: two of W and
+// the same two of W_up), each 16-byte piece of a row used for every token straight from registers, four warps
+// of a block along K (with 1, 2, 4, 8 of them one token takes 10.4, 8.6, 8.7, 8.7 us at 4096 x 4096, 25.2, 22.1, 20.4,
+// 20.8 us at 14336 x 4096 and 15.1, 9.2, 7.4, 8.3 us at 2048 x 7168).  No tensor memory, no ring, no cluster:
+// linear_split_kernel, whose tile has to be set up, drained and joined around the loads, takes 11.4, 22.7 and
+// 10.6 us for these.
+constexpr int LINR_THREADS = 256;
+constexpr int LINR_MAX_TOKENS = 4;
+constexpr int LINR_WK = 4;                          // warps along K
+constexpr int LINR_GROUPS = LINR_THREADS / 32 / LINR_WK;   // and side by side along N
+
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// (lo, hi) += (a.lo b.lo, a.hi b.hi): two fp32 multiply-adds in one instruction
+__device__ __forceinline__ void fma2(unsigned long long& acc, unsigned long long a, unsigned long long b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+// two bf16 as a pair of fp32
+__device__ __forceinline__ unsigned long long bf16x2_pair(uint32_t w) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(w << 16), "r"(w & 0xffff0000u));
+    return r;
+}
+
+template <int MT, bool GATED>
+__global__ void __launch_bounds__(LINR_THREADS, 2)
+linear_rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ W, const uint4* __restrict__ W_up,
+                   const __grid_constant__ LinearParams p) {
+    constexpr int R = 4;                            // weight rows per warp
+    constexpr int RO = GATED ? 2 : 4;               // outputs per warp
+    __shared__ float sums[LINR_THREADS / 32][R * MT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = warp / LINR_WK, kw = warp - g * LINR_WK;
+    const int n_block = blockIdx.x * LINR_GROUPS * RO;
+    const int n0 = n_block + g * RO;
+    const int nvec = p.K >> 3;
+    grid_wait();
+    grid_launch_next();
+    // the thread that will finish an output of a token fetches its operands first
+    const int ft = threadIdx.x / MT, fm = threadIdx.x - ft * MT;   // output of the block, token
+    const int fn = n_block + ft;
+    const bool fin = ft < LINR_GROUPS * RO && fn < p.N && fm < p.M;
+    float bias = 0.0f, bias_up = 0.0f, res = 0.0f;
+    if (fin) {
+        if (p.bias) bias = __ldg(p.bias + fn);
+        if (GATED && p.bias_up) bias_up = __ldg(p.bias_up + fn);
+        if (p.residual) res = __bfloat162float(p.residual[(long long)fm * p.N + fn]);
+    }
+    const uint4* rows[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int n = min(n0 + (GATED ? r & 1 : r), p.N - 1);
+        rows[r] = (GATED && r >= 2 ? W_up : W) + (long long)n * nvec;
+    }
+    const uint4* xr[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) xr[m] = x + (long long)min(m, p.M - 1) * nvec;
+    unsigned long long acc[R][MT];                  // sums over even and over odd K
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[r][m] = 0ull;
+    constexpr int step = LINR_WK * 32;
+    for (int c = kw * 32 + lane; c - lane < nvec; c += 2 * step) {
+        uint4 w[2][R];
+        const bool in[2] = {c < nvec, c + step < nvec};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < R; ++r) w[h][r] = in[h] ? ld_stream(rows[r] + c + h * step) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!in[h]) continue;
+            unsigned long long f[R][4];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                f[r][0] = bf16x2_pair(w[h][r].x);
+                f[r][1] = bf16x2_pair(w[h][r].y);
+                f[r][2] = bf16x2_pair(w[h][r].z);
+                f[r][3] = bf16x2_pair(w[h][r].w);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const uint4 xv = __ldg(xr[m] + c + h * step);
+                const unsigned long long xf[4] = {bf16x2_pair(xv.x), bf16x2_pair(xv.y), bf16x2_pair(xv.z),
+                                                  bf16x2_pair(xv.w)};
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) fma2(acc[r][m], f[r][e], xf[e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const float s = warp_sum(__uint_as_float((uint32_t)acc[r][m]) + __uint_as_float((uint32_t)(acc[r][m] >> 32)));
+            if (lane == 0) sums[warp][r * MT + m] = s;
+        }
+    __syncthreads();
+    if (!fin) return;
+    const int fg = ft / RO, fr = ft - fg * RO;
+    float a = 0.0f, b = 0.0f;
+    #pragma unroll
+    for (int q = 0; q < LINR_WK; ++q) {             // K order
+        a += sums[fg * LINR_WK + q][fr * MT + fm];
+        if (GATED) b += sums[fg * LINR_WK + q][(fr + 2) * MT + fm];
+    }
+    a += bias;
+    a = GATED ? swiglu_f32(a, b + bias_up) : linear_act(p.act, a);
+    p.y[(long long)fm * p.N + fn] = __float2bfloat16_rn(p.residual ? a + res : a);
+}
+
 // ---------------------------------------------------------------- many tokens: persistent CTA pairs
 //
 // Tiles of 256 weight rows x up to 256 tokens by CTA pairs (cta_group::2: each CTA holds 128 weight rows
@@ -430,9 +553,10 @@ constexpr int LINP_CHUNK = 32;                                     // tokens per
 constexpr int LINP_CHUNK_BYTES = LINP_CHUNK * LIN_BM * 4;
 constexpr int LINP_THREADS = 320;                                  // TMA, MMA, 8 epilogue warps
 constexpr int LINP_SMEM_BYTES = LINP_STAGES * LINP_STAGE_BYTES + 2 * LINP_CHUNK_BYTES + 1024 + 256;
-// Token tiles walked together: 16 tiles of 256 tokens at K = 4096 are 33 MB, which stay in L2 while the
-// weights pass by once; all token tiles of M = 16384 would not.
-constexpr int LINP_GROUP = 16;
+// Token tiles walked together: the pairs' tiles of one moment are then about 8 x 9, near the fewest distinct
+// operand rows, and 8 tiles of 256 tokens stay in L2 while the weights pass by (all token tiles of M = 16384
+// would not).  4 to 16 measured alike.
+constexpr int LINP_GROUP = 8;
 
 struct LinearTile {
     int t0, ntok, n_idx;
@@ -457,7 +581,152 @@ __device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&v)[16]
         : "r"(taddr));
 }
 
-// Tensor maps as for linear_split_kernel with CG = 2; bn = 256.
+// Accumulator fragments: 16 tensor-memory lanes x 32 columns.  v[4 i], v[4 i + 1]: lane l / 4, columns
+// 8 i + 2 (l % 4), + 1; v[4 i + 2], v[4 i + 3]: lane l / 4 + 8, the same columns (l: this thread's lane).
+__device__ __forceinline__ void tmem_ld_frag16x32(uint32_t taddr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// One epilogue warp's 32 outputs (a quarter of the CTA's 128) of a tile.  The accumulator is read as 8 x 8
+// fragments (rows: outputs, columns: tokens), finished in registers, and transposed by stmatrix into the
+// warp's 2 KB of shared memory as 32 token rows of 64 bytes, from which 16-byte pieces of whole rows go to
+// y; the residual comes in the other way.  Per 8 outputs that is 4 conversions, one shared-memory
+// instruction each way and an eighth of a global store, against 8 of each with a lane per output (measured on 16384 x
+// 2048 x 512: 68 us so, 105 us through fp32 [token][output] in shared memory).
+// Pieces are XOR-swizzled by row: no bank conflicts.  Rows of y that are not 16-byte aligned (N % 8) are
+// moved an element per lane.
+template <bool F8>
+struct LinearWarp {
+    float bias[4], sw[4];     // of outputs l / 4 + 8 b, b = 0..3
+    int n, nvalid;            // first output; how many of the 32 exist
+    bool vec;
+    uint8_t* stage;
+    uint4 rr[4];              // residual of the next 32 tokens: row 8 j + l / 4, piece l % 4
+
+    __device__ __forceinline__ void begin(const LinearParams& p, int first, int lane) {
+        n = first;
+        nvalid = max(0, min(32, p.N - first));
+        vec = (p.N & 7) == 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int o = (lane >> 2) + 8 * b;
+            bias[b] = p.bias && o < nvalid ? __ldg(p.bias + n + o) : 0.0f;
+            sw[b] = F8 && o < nvalid ? __ldg(p.sw + n + o) : 1.0f;
+        }
+    }
+    __device__ __forceinline__ void load_residual(const LinearParams& p, long long token, int cnt, int lane) {
+        const int q = lane & 3;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = 8 * j + (lane >> 2);
+            if (r < cnt && 8 * q < nvalid)
+                rr[j] = *reinterpret_cast<const uint4*>(p.residual + (token + r) * p.N + n + 8 * q);
+        }
+    }
+    // tokens [token, token + cnt) (cnt <= 32) of the tile from the accumulator at taddr; cnt_next: tokens after them
+    __device__ __forceinline__ void chunk(const LinearParams& p, uint32_t taddr, long long token, int cnt, int cnt_next,
+                                          int lane) {
+        uint32_t v[32];
+        __syncwarp();
+        tmem_ld_frag16x32(taddr, v);
+        tmem_ld_frag16x32(taddr + (16u << 16), v + 16);
+        const int q = lane & 3;
+        if (p.residual) {
+            if (vec) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 8 * j + (lane >> 2);
+                    reinterpret_cast<uint4*>(stage)[r * 4 + (q ^ ((r >> 1) & 3))] = rr[j];
+                }
+                load_residual(p, token + 32, cnt_next, lane);
+            } else {
+                const unsigned short* src = reinterpret_cast<const unsigned short*>(p.residual) + token * p.N + n + lane;
+#pragma unroll 8
+                for (int r = 0; r < 32; ++r)
+                    if (r < cnt && lane < nvalid)
+                        reinterpret_cast<unsigned short*>(stage)[r * 32 + (((lane >> 3) ^ ((r >> 1) & 3)) << 3) + (lane & 7)] =
+                            src[(long long)r * p.N];
+            }
+        }
+        tmem_ld_wait();
+        __syncwarp();
+        const uint32_t row = (uint32_t)(lane & 7), blk = (uint32_t)(lane >> 3);   // fragment addresses: row, output block
+        const uint32_t frag = smem_u32(stage) + row * 64u + ((blk ^ ((row >> 1) & 3u)) << 4);
+        float z[32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                       // 8 tokens
+            float2 sx = make_float2(1.0f, 1.0f);
+            if (F8) {
+                const int tok = 8 * i + 2 * (lane & 3);
+                if (tok < cnt) sx.x = __ldg(p.sx + token + tok);
+                if (tok + 1 < cnt) sx.y = __ldg(p.sx + token + tok + 1);
+            }
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {                   // 8 outputs
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float a = __uint_as_float(v[16 * (b >> 1) + 4 * i + 2 * (b & 1) + h]);
+                    if (F8) a *= (h ? sx.y : sx.x) * sw[b];
+                    z[8 * i + 2 * b + h] = a + bias[b];
+                }
+            }
+        }
+        linear_acts(p.act, z);
+        uint32_t out[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t r4[4] = {0u, 0u, 0u, 0u};
+            if (p.residual) ldmatrix_x4_trans(frag + (uint32_t)i * 512u, r4);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                float lo = z[8 * i + 2 * b], hi = z[8 * i + 2 * b + 1];
+                if (p.residual) {
+                    lo += __uint_as_float(r4[b] << 16);
+                    hi += __uint_as_float(r4[b] & 0xffff0000u);
+                }
+                out[i][b] = pack_bf16x2(lo, hi);
+            }
+        }
+        __syncwarp();                                       // the residual (or the last chunk's rows) has been read
+#pragma unroll
+        for (int i = 0; i < 4; ++i) stmatrix_x4_trans(frag + (uint32_t)i * 512u, out[i]);
+        __syncwarp();
+        if (vec) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = 8 * j + (lane >> 2);
+                const uint4 w = reinterpret_cast<const uint4*>(stage)[r * 4 + (q ^ ((r >> 1) & 3))];
+                if (r < cnt && 8 * q < nvalid) *reinterpret_cast<uint4*>(p.y + (token + r) * p.N + n + 8 * q) = w;
+            }
+        } else {
+            unsigned short* dst = reinterpret_cast<unsigned short*>(p.y) + token * p.N + n + lane;
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r)
+                if (r < cnt && lane < nvalid)
+                    dst[(long long)r * p.N] = reinterpret_cast<const unsigned short*>(
+                        stage)[r * 32 + (((lane >> 3) ^ ((r >> 1) & 3)) << 3) + (lane & 7)];
+        }
+        __syncwarp();
+    }
+};
+
+// Tensor maps as for linear_split_kernel with CG = 2.
 template <bool F8, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LINP_THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWup,
@@ -519,6 +788,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         if (lane == 0) {
             const uint64_t pol_w = policy_evict_normal(), pol_x = policy_evict_last();
             const uint32_t full_leader = map_to_cta(full_bar, 0);
+            const uint32_t bytes = 2u * (uint32_t)(LIN_A_BYTES + (p.bn / 2) * 128);
             int stage = 0, issued = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -529,7 +799,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!mbar_wait(empty_bar + stage, phase ^ 1u, abort_flag)) { ok = false; break; }
                     const uint32_t fb = full_leader + (uint32_t)stage * 8u;
-                    if (leader) mbar_arrive_expect_tx(full_bar + stage, 2u * LINP_STAGE_BYTES);
+                    if (leader) mbar_arrive_expect_tx(full_bar + stage, bytes);
                     uint8_t* w_dst = sW + stage * LIN_A_BYTES;
                     tma_load_2d_pair(w_dst, &tmW, fb, kb * KB, n0, pol_w);
                     if (GATED) tma_load_2d_pair(w_dst + 64 * 128, &tmWup, fb, kb * KB, n0, pol_w);
@@ -592,6 +862,32 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         for (int t = pair; t < total; t += npairs) {
             const LinearTile ti = linear_tile(p, t, nt);
             const int n0 = (ti.n_idx * 2 + rank) * FT, nout = min(FT, p.N - n0);
+            if (!GATED) {
+                // each of the two warps of a lane quarter takes half of the tokens
+                const int c0 = half * 128, c1 = min(c0 + 128, ti.ntok);
+                LinearWarp<F8> e;
+                e.begin(p, n0 + sub * 32, lane);
+                e.stage = reinterpret_cast<uint8_t*>(chunk) + (warp - 2) * 2048;
+                if (p.residual && e.vec && c0 < c1) e.load_residual(p, ti.t0 + c0, min(32, c1 - c0), lane);
+                if (p.residual && nout > 0) {
+                    for (int i = tid; i < ti.ntok * 3; i += 256) {   // a row's piece is at most 3 lines
+                        const int tok = i / 3, col = min((i - tok * 3) * 64, nout - 1);
+                        prefetch_l2(p.residual + (long long)(ti.t0 + tok) * p.N + n0 + col);
+                    }
+                }
+                const bool ready = mbar_wait(tfull_bar + acc, acc_phase, abort_flag);
+                if (!__all_sync(0xffffffffu, ready)) break;
+                tc_fence_after();
+                const uint32_t tb = tmem_base + (uint32_t)(acc * GEMM_ACC_COLS) + ((uint32_t)(sub * 32) << 16);
+                for (int c = c0; c < c1; c += 32)
+                    e.chunk(p, tb + c, ti.t0 + c, min(32, c1 - c), min(32, c1 - c - 32), lane);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + (uint32_t)acc * 8u);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+                continue;
+            }
             LinearCols<F8, GATED> cols;
             uint2 ra[2], rb[2];
             const int tk = tid >> 4;

@@ -1354,12 +1354,12 @@ template <bool F8, bool GATED>
 int launch_linear_pair(DeviceInfo* di, const LinearArgs& a, cudaStream_t s) {
     LinearParams p = linear_params(a);
     p.bn = 256;
-    p.mt = (a.M + 255) / 256;
+    p.mt = (a.M + p.bn - 1) / p.bn;
     const int nt = (a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
     const long long tiles = (long long)nt * p.mt;
     if (tiles >= (1ll << 30)) return MOE_ERR_SHAPE;
     CUtensorMap mW, mWup, mX;
-    int rc = linear_maps<F8, GATED>(a, 128, &mW, &mWup, &mX);
+    int rc = linear_maps<F8, GATED>(a, p.bn / 2, &mW, &mWup, &mX);
     if (rc != MOE_OK) return rc;
     if ((rc = linear_smem_attr<linear_pair_kernel<F8, GATED>>()) != MOE_OK) return rc;
     const long long pairs = di->sms / 2;
@@ -1372,9 +1372,29 @@ int launch_linear_pair(DeviceInfo* di, const LinearArgs& a, cudaStream_t s) {
     return MOE_OK;
 }
 
+template <bool GATED>
+int launch_linear_rows(const LinearArgs& a, cudaStream_t s) {
+    const LinearParams p = linear_params(a);
+    const int outs = LINR_GROUPS * (GATED ? 2 : 4);          // outputs per block
+    const unsigned grid = (unsigned)((a.N + outs - 1) / outs);
+    cudaLaunchConfig_t cfg;
+    const LaunchAttrs attrs(&cfg, grid, LINR_THREADS, 0, s, 1);
+    const uint4 *x = static_cast<const uint4*>(a.x), *W = static_cast<const uint4*>(a.W),
+                *U = static_cast<const uint4*>(a.W_up);
+    const cudaError_t e = a.M == 1   ? cudaLaunchKernelEx(&cfg, linear_rows_kernel<1, GATED>, x, W, U, p)
+                          : a.M == 2 ? cudaLaunchKernelEx(&cfg, linear_rows_kernel<2, GATED>, x, W, U, p)
+                                     : cudaLaunchKernelEx(&cfg, linear_rows_kernel<4, GATED>, x, W, U, p);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
+}
+
 template <bool F8, bool GATED>
 int run_linear_as(DeviceInfo* di, const LinearArgs& a, cudaStream_t s) {
-    const int kind = a.M > 1024 ? 3 : 1;
+    const int kind = !F8 && a.M <= LINR_MAX_TOKENS ? 0 : a.M > 1024 ? 3 : 1;
+    if (kind == 0) return launch_linear_rows<GATED>(a, s);
     return kind == 3   ? launch_linear_pair<F8, GATED>(di, a, s)
            : kind == 2 ? launch_linear_split<F8, GATED, 2>(a, s)
                        : launch_linear_split<F8, GATED, 1>(a, s);

@@ -100,6 +100,24 @@ __global__ void wait_selftest_kernel() {
     mbar_wait(&bar, 0, nullptr);   // no arrival will come
 }
 
+// ---------------------------------------------------------------- warp reductions (every lane gets the result)
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
 // ---------------------------------------------------------------- programmatic dependent launch
 // A kernel launched with programmatic stream serialization may start before the kernel in front of it
 // has ended: grid_wait() returns once that kernel has completed and its writes are visible (at once,

@@ -49,22 +49,6 @@ __device__ __forceinline__ bool key64_before(double ka, int ea, double kb, int e
     return ka > kb || (ka == kb && ea < eb);
 }
 
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
-
 // The weights of the selected experts: lane j < k holds slot j's expert (-1: none) and logit.
 // top / total: the row's largest logit and sum of e^(l - top) over its unmasked experts (softmax
 // without renormalisation).  Renormalised weights are ratios of scores, taken relative to the largest
