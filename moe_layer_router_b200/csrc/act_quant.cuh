@@ -13,6 +13,8 @@
 
 #include <cuda_fp8.h>
 
+#include "ptx.cuh"
+
 namespace moe {
 
 // rows of src (bf16, K per row; row r of the output reads src row gather[r] when gather is
@@ -22,6 +24,8 @@ __global__ void __launch_bounds__(256) quant_rows_e4m3_kernel(const uint4* __res
                                                               const int32_t* __restrict__ gather,
                                                               const int32_t* __restrict__ n_rows, int rows, int K,
                                                               uint2* __restrict__ dst, float* __restrict__ scale) {
+    grid_wait();               // at once, unless launched with programmatic stream serialization
+    grid_launch_next();
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     if (row >= rows) return;
@@ -101,6 +105,8 @@ __global__ void __launch_bounds__(QUANT_CTA) quant_rows_e4m3_reg_kernel(
     const int32_t* __restrict__ dest, int k, uint2* __restrict__ dst, float* __restrict__ scale,
     uint2* __restrict__ dst_tok, float* __restrict__ scale_tok) {
     static_assert(TPR == 32 || TPR == 128 || TPR == 256, "a warp, or whole warps of one CTA");
+    grid_wait();               // at once, unless launched with programmatic stream serialization
+    grid_launch_next();
     constexpr int RPC = QUANT_CTA / TPR;            // rows per CTA
     __shared__ float s_max[QUANT_CTA / 32];
     __shared__ int s_dest[RPC][32];

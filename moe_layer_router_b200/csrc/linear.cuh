@@ -5,18 +5,24 @@
 // the fp32 accumulator multiplied by both.  Everything between the product and the one rounding to
 // bf16 is in fp32.
 //
-// linear_split_kernel: the weights are the MMA's M side (D^T = W x^T), so a single token costs no padded
-// 128-row tile.  A tile is 128 CG weight rows by `bn` tokens (a multiple of 16, at most 256), computed by
-// one CTA (CG = 1) or by a pair on two SMs (CG = 2, tcgen05 cta_group::2: each CTA holds 128 weight rows
-// and half of the tokens, which halves the token traffic from L2).  The K range of a tile is cut over
-// `split` such CTAs or pairs of one cluster, which join their partial sums through distributed shared
-// memory in rank order: no workspace, no atomics, the same result every time.  SwiGLU tiles take 64
-// rows of W and the same 64 rows of W_up per CTA.
+// Three kernels, chosen by run_linear_as():
+//   linear_rows_kernel   up to four tokens: a stream of weights through registers
+//   linear_split_kernel  more tokens: 128 weight rows x up to 128 tokens per tile, K cut over a cluster
+//   linear_pair_kernel   many tokens: persistent CTA pairs, 256 weight rows x up to 256 tokens
+// In the last two the weights are the MMA's M side (D^T = W x^T), so few tokens cost no padded 128-row tile and
+// the token tile can be any multiple of 16.  SwiGLU tiles take 64 rows of W and the same 64 of W_up per CTA.
 //
-// Warp roles (256 threads): warp 0 TMA producer, warp 1 tensor memory + MMA issuer, warps 2-3 bring the
+// linear_split_kernel: the K range of a tile is cut over the `split` CTAs of a cluster, which join their partial
+// sums through distributed shared memory in rank order: no workspace, no atomics, the same result every
+// time.  Warp roles (256 threads): warp 0 TMA producer, warp 1 tensor memory + MMA issuer, warps 2-3 bring the
 // epilogue's operands into L2.  Then all eight warps move the accumulator (a lane per output, a column per
-// token) to shared memory as fp32 [slice][token][128], each token's sums to the rank of the cluster
-// that owns the token, and each rank adds the slices of its tokens, applies the epilogue and stores.
+// token) to shared memory as fp32 [slice][token][128], each token's sums to the rank of the cluster that owns
+// the token, and each rank adds the slices of its tokens, applies the epilogue and stores.  What bounds it: the
+// weights' stream for few tokens (14336 x 4096, 16 tokens: 23.3 us, 5.0 of 6.46 TB/s), the operands' way from
+// L2 for hundreds (512 x 4096 x 4096: 25 us, 32 KB per 128 x 128 x 64 products at about 75 B per clock and SM);
+// setting up, handing over and joining take about 4 us besides.  Tried: pairs of CTAs (cta_group::2) in this
+// kernel, which halve the token traffic, won or lost under 10 % at 128 to 1024 tokens; prefetching weights into L2
+// ahead of the ring cost 5 to 20 %.
 #pragma once
 
 #include "grouped_gemm.cuh"
@@ -29,7 +35,6 @@ enum { LIN_NONE = 0, LIN_RELU = 1, LIN_SILU = 2, LIN_GELU = 3, LIN_GELU_TANH = 4
 constexpr int LIN_BM = 128;                        // weight rows per tile
 constexpr int LIN_A_BYTES = LIN_BM * 128;          // one stage of weights: 128-byte rows
 constexpr int LIN_THREADS = 256;
-constexpr int LIN_MAX_STAGES = 8;
 constexpr int LIN_MAX_SPLIT = 8;                   // portable cluster size
 
 struct LinearParams {
@@ -48,9 +53,8 @@ struct LinearParams {
 
 // Partial sums of a CTA: `split` slices of ceil(ntok / split) tokens, at most bn + split - 1 rows.
 __host__ __device__ constexpr int linear_part_bytes(int bn, int split) { return (bn + split) * LIN_BM * 4; }
-// x_rows: token rows that one CTA loads per stage (bn / CG)
-__host__ __device__ constexpr int linear_smem_bytes(int stages, int x_rows, int own_part_bytes) {
-    return stages * (LIN_A_BYTES + x_rows * 128) + own_part_bytes + 1024 + 256;
+__host__ __device__ constexpr int linear_smem_bytes(int stages, int bn, int own_part_bytes) {
+    return stages * (LIN_A_BYTES + bn * 128) + own_part_bytes + 1024 + 256;
 }
 
 // Activation of a pre-activation z (not SwiGLU).  gelu: z times the normal distribution function,
@@ -221,15 +225,15 @@ __device__ __forceinline__ void linear_join(const LinearParams& p, const float* 
     }
 }
 
-// tcgen05 shapes: M = 128 CG, N = bn; tensor maps: W / W_up with boxes of 128 rows (SwiGLU: 64), x with
-// boxes of bn / CG rows.  grid = tiles * split * CG, cluster = the split * CG CTAs of one tile.
-template <bool F8, bool GATED, int CG>
+// tcgen05 shapes: M = 128, N = bn; tensor maps: W / W_up with boxes of 128 rows (SwiGLU: 64), x with boxes of bn
+// rows.  grid = tiles * split, cluster = the split CTAs of one tile.
+template <bool F8, bool GATED>
 __global__ void __launch_bounds__(LIN_THREADS)
 linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWup,
                     const __grid_constant__ CUtensorMap tmX, const __grid_constant__ LinearParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int S = p.stages, x_rows = p.bn / CG, x_bytes = x_rows * 128;
+    const int S = p.stages, x_bytes = p.bn * 128;
     uint8_t* sW = smem;
     uint8_t* sX = smem + S * LIN_A_BYTES;
     // partial sums: over the ring, or (small tiles) in shared memory of their own, where another rank may
@@ -242,19 +246,16 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int csize = p.split * CG;
-    const int tile = blockIdx.x / csize, rank = blockIdx.x - tile * csize;   // = the rank in the cluster
-    const int slice = rank / CG, cta = rank - slice * CG;                    // K slice; CTA of its pair
-    const bool leader = cta == 0;
+    const int tile = blockIdx.x / p.split, slice = blockIdx.x - tile * p.split;   // K slice = cluster rank
     const int m_idx = tile % p.mt, n_idx = tile / p.mt;
     constexpr int FT = GATED ? 64 : 128;           // outputs per CTA
-    const int n0 = (n_idx * CG + cta) * FT;
+    const int n0 = n_idx * FT;
     const int t0 = m_idx * p.bn;                   // first token
     const int ntok = min(p.bn, p.M - t0);
     constexpr int KB = F8 ? 128 : 64;              // K elements per 128-byte stage row
     const int nk = (p.K + KB - 1) / KB;
     const int kb0 = (int)((long long)nk * slice / p.split), kb1 = (int)((long long)nk * (slice + 1) / p.split);
-    const int nout = min(FT, p.N - n0);            // <= 0: a pair's second CTA past the last output
+    const int nout = min(FT, p.N - n0);
     const int own = (ntok + p.split - 1) / p.split;               // tokens joined by each slice's rank
     const int my_t0 = min(slice * own, ntok), my_ntok = min(own, ntok - my_t0);
 
@@ -273,19 +274,12 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
         if (GATED) prefetch_tensormap(&tmWup);
     }
     if (warp == 1) {
-        if (CG == 2) {
-            tmem_alloc_pair(tmem_slot, p.tmem_cols);
-            tmem_relinquish_pair();
-        } else {
-            tmem_alloc(tmem_slot, p.tmem_cols);
-            tmem_relinquish();
-        }
+        tmem_alloc(tmem_slot, p.tmem_cols);
+        tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
-    // every CTA of the cluster runs, and a pair's barriers are initialised, before remote accesses
-    if (CG == 2) cluster_sync_all();
-    else if (p.split > 1) cluster_arrive();
+    if (p.split > 1) cluster_arrive();             // waited for before the first remote store
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     grid_wait();
@@ -295,38 +289,28 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
         if (lane == 0) {
             const uint64_t pol_w = p.mt == 1 ? policy_evict_first() : policy_evict_normal();
             const uint64_t pol_x = policy_evict_last();
-            const uint32_t bytes = CG * (LIN_A_BYTES + (uint32_t)x_bytes);   // of both CTAs of a pair
-            const uint32_t full_leader = map_to_cta(full_bar, (uint32_t)(rank - cta));
+            const uint32_t bytes = LIN_A_BYTES + (uint32_t)x_bytes;
             int issued = 0;
             bool ok = true;
             for (int kb = kb0; kb < kb1; ++kb) {
                 const int s = issued % S;
                 if (!mbar_wait(empty_bar + s, ((issued / S) & 1) ^ 1u, abort_flag)) { ok = false; break; }
-                if (leader) mbar_arrive_expect_tx(full_bar + s, bytes);
+                mbar_arrive_expect_tx(full_bar + s, bytes);
                 uint8_t* w_dst = sW + s * LIN_A_BYTES;
-                const int tx = t0 + cta * x_rows;
-                if (CG == 2) {
-                    const uint32_t fb = full_leader + (uint32_t)s * 8u;
-                    tma_load_2d_pair(w_dst, &tmW, fb, kb * KB, n0, pol_w);
-                    if (GATED) tma_load_2d_pair(w_dst + 64 * 128, &tmWup, fb, kb * KB, n0, pol_w);
-                    tma_load_2d_pair(sX + s * x_bytes, &tmX, fb, kb * KB, tx, pol_x);
-                } else {
-                    tma_load_2d(w_dst, &tmW, full_bar + s, kb * KB, n0, pol_w);
-                    if (GATED) tma_load_2d(w_dst + 64 * 128, &tmWup, full_bar + s, kb * KB, n0, pol_w);
-                    tma_load_2d(sX + s * x_bytes, &tmX, full_bar + s, kb * KB, tx, pol_x);
-                }
+                tma_load_2d(w_dst, &tmW, full_bar + s, kb * KB, n0, pol_w);
+                if (GATED) tma_load_2d(w_dst + 64 * 128, &tmWup, full_bar + s, kb * KB, n0, pol_w);
+                tma_load_2d(sX + s * x_bytes, &tmX, full_bar + s, kb * KB, t0, pol_x);
                 ++issued;
             }
-            if (!ok && leader) {
+            if (!ok) {
                 const int n = issued < S ? issued : S;      // copies in flight land before exit
                 for (int i = 1; i <= n; ++i)
                     mbar_wait(full_bar + ((issued - i) % S), (uint32_t)(((issued - i) / S) & 1), nullptr);
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
-            const uint32_t idesc = F8 ? idesc_e4m3_f32(LIN_BM * CG, p.bn) : idesc_bf16_f32(LIN_BM * CG, p.bn);
-            const uint16_t both = (uint16_t)(3u << rank);    // this CTA and its peer
+        if (lane == 0) {
+            const uint32_t idesc = F8 ? idesc_e4m3_f32(LIN_BM, p.bn) : idesc_bf16_f32(LIN_BM, p.bn);
             for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
                 const int s = i % S;
                 if (!mbar_wait(full_bar + s, (i / S) & 1, abort_flag)) break;
@@ -335,25 +319,17 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
                 const uint64_t bd = smem_desc_k_sw128(sX + s * x_bytes);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                    if (CG == 2) {
-                        if (F8) umma_e4m3_pair(tmem_base, ad + 2ull * kk, bd + 2ull * kk, idesc, (i | kk) != 0);
-                        else umma_bf16_pair(tmem_base, ad + 2ull * kk, bd + 2ull * kk, idesc, (i | kk) != 0);
-                    } else {
-                        if (F8) umma_e4m3(tmem_base, ad + 2ull * kk, bd + 2ull * kk, idesc, (i | kk) != 0);
-                        else umma_bf16(tmem_base, ad + 2ull * kk, bd + 2ull * kk, idesc, (i | kk) != 0);
-                    }
+                    if (F8) umma_e4m3(tmem_base, ad + 2ull * kk, bd + 2ull * kk, idesc, (i | kk) != 0);
+                    else umma_bf16(tmem_base, ad + 2ull * kk, bd + 2ull * kk, idesc, (i | kk) != 0);
                 }
-                if (CG == 2) umma_commit_pair(empty_bar + s, both);
-                else umma_commit(empty_bar + s);
+                umma_commit(empty_bar + s);
             }
-            // all MMAs retired: the accumulator is final, the ring is idle
-            if (CG == 2) umma_commit_pair(done_bar, both);
-            else umma_commit(done_bar);
+            umma_commit(done_bar);       // all MMAs retired: the accumulator is final, the ring is idle
             mbar_wait(done_bar, 0, nullptr);
         }
     } else if (warp < 4) {
         const int tid = threadIdx.x - 64;
-        if (p.residual && nout > 0) {                            // a row's segment is at most 3 lines of 128 bytes
+        if (p.residual) {                                        // a row's segment is at most 3 lines of 128 bytes
             for (int i = tid; i < my_ntok * 3; i += 64) {
                 const int tok = i / 3, col = min((i - tok * 3) * 64, nout - 1);
                 prefetch_l2(p.residual + (long long)(t0 + my_t0 + tok) * p.N + n0 + col);
@@ -367,7 +343,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
         }
     }
     __syncwarp();
-    if (CG == 1 && p.split > 1) cluster_wait();                  // the arrival at the start
+    if (p.split > 1) cluster_wait();                             // every CTA of the cluster runs
     const bool ready = __all_sync(0xffffffffu, mbar_wait(done_bar, 0, nullptr));
     if (p.split > 1 && !p.own_part) cluster_sync_all();          // every rank's ring is idle
     if (ready) {
@@ -386,7 +362,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
                     if (c + j < ntok) part[(c + j) * LIN_BM + sub * 32 + lane] = __uint_as_float(v[j]);
             } else {
                 int q = c / own, in_q = c - q * own;             // the owner of column c, and its place there
-                uint32_t at = map_to_cta_addr(part0, (uint32_t)(cta + CG * q)) + (uint32_t)(slice * own) * (LIN_BM * 4);
+                uint32_t at = map_to_cta_addr(part0, (uint32_t)q) + (uint32_t)(slice * own) * (LIN_BM * 4);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     if (c + j < ntok) st_cluster_f1(at + (uint32_t)in_q * (LIN_BM * 4), __uint_as_float(v[j]));
@@ -394,7 +370,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
                         in_q = 0;
                         ++q;
                         if (c + j + 1 < ntok)
-                            at = map_to_cta_addr(part0, (uint32_t)(cta + CG * q)) + (uint32_t)(slice * own) * (LIN_BM * 4);
+                            at = map_to_cta_addr(part0, (uint32_t)q) + (uint32_t)(slice * own) * (LIN_BM * 4);
                     }
                 }
             }
@@ -402,14 +378,13 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
         tc_fence_before();
     }
     __syncwarp();
-    if (CG * p.split > 1) cluster_sync_all();                    // all partial sums have arrived
+    if (p.split > 1) cluster_sync_all();                         // all partial sums have arrived
     else __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        if (CG == 2) tmem_dealloc_pair(tmem_base, p.tmem_cols);
-        else tmem_dealloc(tmem_base, p.tmem_cols);
+        tmem_dealloc(tmem_base, p.tmem_cols);
     }
-    if (nout <= 0 || my_ntok <= 0) return;
+    if (my_ntok <= 0) return;
     const long long first = t0 + my_t0;
     if (p.split == 1) linear_join<F8, GATED, 1>(p, part, own, first, my_ntok, n0, nout, threadIdx.x);
     else if (p.split == 2) linear_join<F8, GATED, 2>(p, part, own, first, my_ntok, n0, nout, threadIdx.x);
@@ -726,7 +701,7 @@ struct LinearWarp {
     }
 };
 
-// Tensor maps as for linear_split_kernel with CG = 2.
+// Tensor maps as for linear_split_kernel, x with boxes of bn / 2 rows.
 template <bool F8, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LINP_THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWup,

@@ -1318,32 +1318,39 @@ int linear_smem_attr() {
     return MOE_OK;
 }
 
-template <bool F8, bool GATED, int CG>
+// Tiles of linear_split_kernel.  Token tiles: one up to 128 tokens, then tiles of about 128; short K (up to
+// 24 k-blocks) prefers tiles of 64, whose sums are joined sooner (512 x 512, 512 tokens: 5.6 us against 6.8).
+// K slices: doubled while the tiles do not fill two CTAs per SM and each slice keeps 2 k-blocks, beyond 128 CTAs
+// only while it keeps 14 (32 tiles at K = 4096, 16 tokens: 4 slices 11.0 us, 8 11.4; at K = 14336: 26.4,
+// 23.9).  Over 290 combinations of sizes and types this rule is 3 % off the best of all tiles and slices.
+template <bool F8, bool GATED>
 int launch_linear_split(const LinearArgs& a, cudaStream_t s) {
     LinearParams p = linear_params(a);
-    // token tiles of equal size (multiples of 16)
-    const int mt0 = (a.M + 255) / 256;
+    const int nt = (a.N + (GATED ? 63 : 127)) / (GATED ? 64 : 128);
+    const int nk = (a.K + (F8 ? 127 : 63)) / (F8 ? 128 : 64);
+    const int mt0 = a.M <= 64 ? 1 : nk <= 24 && a.M <= 1024 ? (a.M + 63) / 64 : (a.M + 127) / 128;
     p.bn = ((a.M + mt0 - 1) / mt0 + 15) / 16 * 16;
     p.mt = (a.M + p.bn - 1) / p.bn;
-    p.tmem_cols = p.bn <= 32 ? 32 : p.bn <= 64 ? 64 : p.bn <= 128 ? 128 : 256;
-    constexpr int FT = (GATED ? 64 : 128) * CG;
-    const int nt = (a.N + FT - 1) / FT;
-    const int nk = (a.K + (F8 ? 127 : 63)) / (F8 ? 128 : 64);
-    p.stages = 4;
-    p.split = 1;
-    p.own_part = p.split > 1 && p.bn <= 32;
-    while (!p.own_part && p.stages * (LIN_A_BYTES + p.bn / CG * 128) < linear_part_bytes(p.bn, p.split)) ++p.stages;
+    p.tmem_cols = p.bn <= 32 ? 32 : p.bn <= 64 ? 64 : 128;
     const long long tiles = (long long)nt * p.mt;
-    if (tiles * p.split * CG >= (1ll << 31)) return MOE_ERR_SHAPE;
-    (void)nk;
+    p.split = 1;
+    while (p.split < LIN_MAX_SPLIT && tiles * p.split * 2 <= 256 && nk / (p.split * 2) >= 2 &&
+           (tiles * p.split < 128 || nk / (p.split * 2) >= 14))
+        p.split *= 2;
+    p.own_part = p.split > 1 && p.bn <= 32;
+    // a ring that leaves room for two CTAs per SM, and holds the partial sums
+    p.stages = 4 * (LIN_A_BYTES + p.bn * 128) <= 112000 ? 4 : 3;
+    while (!p.own_part && p.stages * (LIN_A_BYTES + p.bn * 128) < linear_part_bytes(p.bn, p.split)) ++p.stages;
+    if (tiles * p.split >= (1ll << 31)) return MOE_ERR_SHAPE;
     CUtensorMap mW, mWup, mX;
-    int rc = linear_maps<F8, GATED>(a, p.bn / CG, &mW, &mWup, &mX);
+    int rc = linear_maps<F8, GATED>(a, p.bn, &mW, &mWup, &mX);
     if (rc != MOE_OK) return rc;
-    if ((rc = linear_smem_attr<linear_split_kernel<F8, GATED, CG>>()) != MOE_OK) return rc;
+    if ((rc = linear_smem_attr<linear_split_kernel<F8, GATED>>()) != MOE_OK) return rc;
     cudaLaunchConfig_t cfg;
-    const LaunchAttrs attrs(&cfg, (unsigned)(tiles * p.split * CG), LIN_THREADS,
-                            linear_smem_bytes(p.stages, p.bn / CG, p.own_part ? linear_part_bytes(p.bn, p.split) : 0), s, p.split * CG);
-    if (cudaLaunchKernelEx(&cfg, linear_split_kernel<F8, GATED, CG>, mW, mWup, mX, p) != cudaSuccess) {
+    const LaunchAttrs attrs(&cfg, (unsigned)(tiles * p.split), LIN_THREADS,
+                            linear_smem_bytes(p.stages, p.bn, p.own_part ? linear_part_bytes(p.bn, p.split) : 0), s,
+                            p.split);
+    if (cudaLaunchKernelEx(&cfg, linear_split_kernel<F8, GATED>, mW, mWup, mX, p) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
@@ -1353,16 +1360,27 @@ int launch_linear_split(const LinearArgs& a, cudaStream_t s) {
 template <bool F8, bool GATED>
 int launch_linear_pair(DeviceInfo* di, const LinearArgs& a, cudaStream_t s) {
     LinearParams p = linear_params(a);
-    p.bn = 256;
-    p.mt = (a.M + p.bn - 1) / p.bn;
     const int nt = (a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
+    // tokens per tile: the fewest cycles over whole waves of pairs, a k-block taking 2 bn cycles of products or
+    // 16 KB of weights and 64 bn bytes of tokens at about 70 B per clock (2048 x 4096 x 4096 is two waves either
+    // way: 54.8 us at 256, 51.3 at 240)
+    const long long pairs = di->sms / 2;
+    long long best = -1;
+    for (int bn = 256; bn >= 128; bn -= 16) {
+        const long long t = (long long)nt * ((a.M + bn - 1) / bn), waves = (t + pairs - 1) / pairs;
+        const long long cost = waves * (std::max(2 * bn, (16384 + 64 * bn) / 70) + 64);
+        if (best < 0 || cost < best) {
+            best = cost;
+            p.bn = bn;
+        }
+    }
+    p.mt = (a.M + p.bn - 1) / p.bn;
     const long long tiles = (long long)nt * p.mt;
     if (tiles >= (1ll << 30)) return MOE_ERR_SHAPE;
     CUtensorMap mW, mWup, mX;
     int rc = linear_maps<F8, GATED>(a, p.bn / 2, &mW, &mWup, &mX);
     if (rc != MOE_OK) return rc;
     if ((rc = linear_smem_attr<linear_pair_kernel<F8, GATED>>()) != MOE_OK) return rc;
-    const long long pairs = di->sms / 2;
     cudaLaunchConfig_t cfg;
     const LaunchAttrs attrs(&cfg, 2 * (unsigned)std::min(tiles, pairs), LINP_THREADS, LINP_SMEM_BYTES, s, 1);
     if (cudaLaunchKernelEx(&cfg, linear_pair_kernel<F8, GATED>, mW, mWup, mX, p) != cudaSuccess) {
@@ -1391,18 +1409,63 @@ int launch_linear_rows(const LinearArgs& a, cudaStream_t s) {
     return MOE_OK;
 }
 
+// Which kernel.  Rows: one or two tokens always, three and four while the weights are few (4096 x 4096: 10.1 us
+// against 11.4; 14336 x 4096: 30.2 against 22.6, its multiply-adds then take longer than the loads).  Pairs: once
+// their tiles fill most of the GPU's 74 pairs, or for short K from 1024 tokens on (768 x 4096 x 4096: 30 us
+// against 38; 512: 27.2 against 25.0; 1536 x 1000 x 1384: 15.7 against 18.5).
 template <bool F8, bool GATED>
 int run_linear_as(DeviceInfo* di, const LinearArgs& a, cudaStream_t s) {
-    const int kind = !F8 && a.M <= LINR_MAX_TOKENS ? 0 : a.M > 1024 ? 3 : 1;
-    if (kind == 0) return launch_linear_rows<GATED>(a, s);
-    return kind == 3   ? launch_linear_pair<F8, GATED>(di, a, s)
-           : kind == 2 ? launch_linear_split<F8, GATED, 2>(a, s)
-                       : launch_linear_split<F8, GATED, 1>(a, s);
+    const long long elems = (long long)a.N * a.K * (GATED ? 2 : 1);
+    if constexpr (!F8) {
+        if (a.M <= 2 || (a.M <= LINR_MAX_TOKENS && elems <= (1ll << 24))) return launch_linear_rows<GATED>(a, s);
+    }
+    const long long tiles = (long long)((a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256)) * ((a.M + 255) / 256);
+    const int nk = (a.K + (F8 ? 127 : 63)) / (F8 ? 128 : 64);
+    if (a.M > 128 && (tiles >= 40 || (tiles >= 16 && nk <= 24 && a.M >= 1024)))
+        return launch_linear_pair<F8, GATED>(di, a, s);
+    return launch_linear_split<F8, GATED>(a, s);
 }
 
 template <bool F8>
 int run_linear(DeviceInfo* di, const LinearArgs& a, cudaStream_t s) {
     return a.act == MOE_ACT_SWIGLU ? run_linear_as<F8, true>(di, a, s) : run_linear_as<F8, false>(di, a, s);
+}
+
+// x rows -> e4m3 codes and scales, as run_quant_h() does for long and short rows, launched with programmatic
+// stream serialization so that neither this kernel nor the product after it waits out a launch.
+int quant_linear_x(const LinearArgs& a, uint8_t* xq, float* sx, cudaStream_t s) {
+    const int chunks = a.K / 8;
+    const uint4* x = static_cast<const uint4*>(a.x);
+    uint2* d = reinterpret_cast<uint2*>(xq);
+    const int32_t* none = nullptr;
+    uint2* no_codes = nullptr;
+    float* no_scale = nullptr;
+    cudaLaunchConfig_t cfg;
+    cudaError_t e;
+#define MOE_QUANT(TPR, C)                                                                                          \
+    do {                                                                                                           \
+        const LaunchAttrs attrs(&cfg, (unsigned)(((long long)a.M * TPR + QUANT_CTA - 1) / QUANT_CTA), QUANT_CTA, 0, \
+                                s, 1);                                                                             \
+        e = cudaLaunchKernelEx(&cfg, quant_rows_e4m3_reg_kernel<TPR, C>, x, none, (long long)a.M, a.K, none, 0, d, \
+                               sx, no_codes, no_scale);                                                            \
+    } while (0)
+    if (a.M > 256 && a.K <= 2048) {      // many short rows: two passes with few registers
+        const LaunchAttrs attrs(&cfg, (unsigned)((a.M + 7) / 8), 256, 0, s, 1);
+        e = cudaLaunchKernelEx(&cfg, quant_rows_e4m3_kernel, x, none, none, a.M, a.K, d, sx);
+    } else if (chunks <= 128 * 2) MOE_QUANT(128, 2);
+    else if (chunks <= 128 * 4) MOE_QUANT(128, 4);
+    else if (chunks <= 128 * 8) MOE_QUANT(128, 8);
+    else if (chunks <= 256 * 8) MOE_QUANT(256, 8);
+    else {
+        const LaunchAttrs attrs(&cfg, (unsigned)((a.M + 7) / 8), 256, 0, s, 1);
+        e = cudaLaunchKernelEx(&cfg, quant_rows_e4m3_kernel, x, none, none, a.M, a.K, d, sx);
+    }
+#undef MOE_QUANT
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
 }
 
 size_t linear_scale_offset(int M, int K) { return align256((size_t)M * K); }
@@ -1444,8 +1507,9 @@ int moe_linear_w8a8(const moe_bf16* x, const uint8_t* Wq, const float* s, const 
     uint8_t* xq = static_cast<uint8_t*>(ws);
     float* sx = reinterpret_cast<float*>(xq + linear_scale_offset(M, K));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((rc = run_quant_h(x, nullptr, M, K, xq, sx, st)) != MOE_OK) return rc;
-    const LinearArgs a = {xq, Wq, Wq_up, sx, s, s_up, bias, bias_up, residual, M, N, K, act, y};
+    LinearArgs a = {x, Wq, Wq_up, sx, s, s_up, bias, bias_up, residual, M, N, K, act, y};
+    if ((rc = quant_linear_x(a, xq, sx, st)) != MOE_OK) return rc;
+    a = {xq, Wq, Wq_up, sx, s, s_up, bias, bias_up, residual, M, N, K, act, y};
     return run_linear<true>(di, a, st);
 }
 
