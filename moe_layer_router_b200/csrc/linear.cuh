@@ -518,16 +518,13 @@ linear_rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ W, con
 //
 // Tiles of 256 weight rows x up to 256 tokens by CTA pairs (cta_group::2: each CTA holds 128 weight rows
 // and half of the tokens: 32 KB of operands per 64 K-elements for 256 x 128 outputs per SM), a 6-stage
-// ring and two accumulators, so that a tile's epilogue runs under the next tile's products.  The eight
-// epilogue warps move 32 tokens of the accumulator at a time to shared memory (double buffered), then
-// each thread finishes its outputs of two tokens, the residual of the next 32 already on its way.
+// ring and two accumulators, so that a tile's epilogue runs under the next tile's products.
 // The last token tile runs its MMAs with N = its tokens rounded up to 16.
 constexpr int LINP_STAGES = 6;
 constexpr int LINP_STAGE_BYTES = LIN_A_BYTES + 128 * 128;          // 128 weight rows + 128 tokens
-constexpr int LINP_CHUNK = 32;                                     // tokens per epilogue step
-constexpr int LINP_CHUNK_BYTES = LINP_CHUNK * LIN_BM * 4;
+constexpr int LINP_EPI_BYTES = 8 * 2 * 2048;                       // two 2 KB buffers per epilogue warp
 constexpr int LINP_THREADS = 320;                                  // TMA, MMA, 8 epilogue warps
-constexpr int LINP_SMEM_BYTES = LINP_STAGES * LINP_STAGE_BYTES + 2 * LINP_CHUNK_BYTES + 1024 + 256;
+constexpr int LINP_SMEM_BYTES = LINP_STAGES * LINP_STAGE_BYTES + LINP_EPI_BYTES + 1024 + 256;
 // Token tiles walked together: the pairs' tiles of one moment are then about 8 x 9, near the fewest distinct
 // operand rows, and 8 tiles of 256 tokens stay in L2 while the weights pass by (all token tiles of M = 16384
 // would not).  4 to 16 measured alike.
@@ -545,15 +542,6 @@ __device__ __forceinline__ LinearTile linear_tile(const LinearParams& p, int t, 
     r.t0 = (m0 + in - r.n_idx * gm) * p.bn;
     r.ntok = min(p.bn, p.M - r.t0);
     return r;
-}
-
-__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr));
 }
 
 // Accumulator fragments: 16 tensor-memory lanes x 32 columns.  v[4 i], v[4 i + 1]: lane l / 4, columns
@@ -578,74 +566,93 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                  : "memory");
 }
 
-// One epilogue warp's 32 outputs (a quarter of the CTA's 128) of a tile.  The accumulator is read as 8 x 8
-// fragments (rows: outputs, columns: tokens), finished in registers, and transposed by stmatrix into the
-// warp's 2 KB of shared memory as 32 token rows of 64 bytes, from which 16-byte pieces of whole rows go to
-// y; the residual comes in the other way.  Per 8 outputs that is 4 conversions, one shared-memory
-// instruction each way and an eighth of a global store, against 8 of each with a lane per output (measured on 16384 x
-// 2048 x 512: 68 us so, 105 us through fp32 [token][output] in shared memory).
-// Pieces are XOR-swizzled by row: no bank conflicts.  Rows of y that are not 16-byte aligned (N % 8) are
-// moved an element per lane.
-template <bool F8>
+// One epilogue warp's 32 accumulator lanes of a tile.  The accumulator is read as 8 x 8 fragments (rows: outputs,
+// columns: tokens), finished in registers, and transposed by stmatrix into 2 KB of shared memory as token rows
+// of 64 bytes, from which 16-byte pieces of whole rows go to y; the residual comes in the other way.  Per 8
+// outputs that is 4 conversions, one shared-memory instruction each way and an eighth of a global store; with a lane
+// per output each of these was 8 instructions (16384 x 2048 x 512 with residual: 61 us this way, 68 us a lane per
+// output, 105 us through fp32 [token][output] in shared memory).  Pieces are XOR-swizzled by row: no bank conflicts.
+// Rows of y that are not 16-byte aligned (N % 8) are moved an element per lane.
+// GATED: lanes 0-63 of the CTA's accumulator hold x W^T, lanes 64-127 x W_up^T of the same 64 outputs.  The two
+// warps of a pair swap halves of every 32 tokens (through the other's 2 KB, two of them in turn) and each finishes
+// 16 tokens.
+template <bool F8, bool GATED>
 struct LinearWarp {
+    static constexpr int NB = GATED ? 2 : 4;   // blocks of 8 tokens that this warp finishes, of the chunk's 4
     float bias[4], sw[4];     // of outputs l / 4 + 8 b, b = 0..3
     int n, nvalid;            // first output; how many of the 32 exist
+    int own;                  // first of this warp's tokens in a chunk
     bool vec;
-    uint8_t* stage;
-    uint4 rr[4];              // residual of the next 32 tokens: row 8 j + l / 4, piece l % 4
+    uint4 rr[NB];             // residual of the next tokens: row 8 j + l / 4, piece l % 4
 
-    __device__ __forceinline__ void begin(const LinearParams& p, int first, int lane) {
+    __device__ __forceinline__ void begin(const LinearParams& p, int first, bool up, int lane) {
         n = first;
         nvalid = max(0, min(32, p.N - first));
+        own = up ? 16 : 0;
         vec = (p.N & 7) == 0;
+        const float* bp = up ? p.bias_up : p.bias;
+        const float* sp = up ? p.sw_up : p.sw;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const int o = (lane >> 2) + 8 * b;
-            bias[b] = p.bias && o < nvalid ? __ldg(p.bias + n + o) : 0.0f;
-            sw[b] = F8 && o < nvalid ? __ldg(p.sw + n + o) : 1.0f;
+            bias[b] = bp && o < nvalid ? __ldg(bp + n + o) : 0.0f;
+            sw[b] = F8 && o < nvalid ? __ldg(sp + n + o) : 1.0f;
         }
     }
+    // cnt: tokens of the chunk that starts at `token`
     __device__ __forceinline__ void load_residual(const LinearParams& p, long long token, int cnt, int lane) {
         const int q = lane & 3;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = 8 * j + (lane >> 2);
+        for (int j = 0; j < NB; ++j) {
+            const int r = own + 8 * j + (lane >> 2);
             if (r < cnt && 8 * q < nvalid)
                 rr[j] = *reinterpret_cast<const uint4*>(p.residual + (token + r) * p.N + n + 8 * q);
         }
     }
-    // tokens [token, token + cnt) (cnt <= 32) of the tile from the accumulator at taddr; cnt_next: tokens after them
+    // The residual of this warp's tokens of the chunk at `token` into its rows in shared memory; VEC: from rr, and
+    // the next chunk's into rr.
+    template <bool VEC>
+    __device__ __forceinline__ void stage_residual(const LinearParams& p, long long token, int rows, int cnt_next,
+                                                   int lane, uint8_t* mine) {
+        if (VEC) {
+            const int q = lane & 3;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const int r = 8 * j + (lane >> 2);
+                reinterpret_cast<uint4*>(mine)[r * 4 + (q ^ ((r >> 1) & 3))] = rr[j];
+            }
+            load_residual(p, token + 32, cnt_next, lane);
+        } else if (nvalid > 0 && rows > 0) {      // 16 loads at a time; masked ones repeat the last element
+            const unsigned short* src = reinterpret_cast<const unsigned short*>(p.residual) + (token + own) * p.N + n +
+                                        min(lane, nvalid - 1);
+#pragma unroll 1
+            for (int r0 = 0; r0 < 8 * NB; r0 += 16) {
+                unsigned short u[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) u[r] = src[(long long)min(r0 + r, rows - 1) * p.N];
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    reinterpret_cast<unsigned short*>(mine)[(r0 + r) * 32 + (((lane >> 3) ^ ((r >> 1) & 3)) << 3) +
+                                                            (lane & 7)] = u[r];
+            }
+        }
+    }
+    // tokens [token, token + cnt), 1 <= cnt <= 32, from the accumulator at taddr; cnt_next: tokens after them.
+    // mine / other: 2 KB of this warp / of its partner; bar: the pair's barrier; VEC: `vec`
+    template <bool VEC>
     __device__ __forceinline__ void chunk(const LinearParams& p, uint32_t taddr, long long token, int cnt, int cnt_next,
-                                          int lane) {
+                                          int lane, uint8_t* mine, uint8_t* other, int bar) {
         uint32_t v[32];
         __syncwarp();
         tmem_ld_frag16x32(taddr, v);
         tmem_ld_frag16x32(taddr + (16u << 16), v + 16);
         const int q = lane & 3;
-        if (p.residual) {
-            if (vec) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = 8 * j + (lane >> 2);
-                    reinterpret_cast<uint4*>(stage)[r * 4 + (q ^ ((r >> 1) & 3))] = rr[j];
-                }
-                load_residual(p, token + 32, cnt_next, lane);
-            } else {
-                const unsigned short* src = reinterpret_cast<const unsigned short*>(p.residual) + token * p.N + n + lane;
-#pragma unroll 8
-                for (int r = 0; r < 32; ++r)
-                    if (r < cnt && lane < nvalid)
-                        reinterpret_cast<unsigned short*>(stage)[r * 32 + (((lane >> 3) ^ ((r >> 1) & 3)) << 3) + (lane & 7)] =
-                            src[(long long)r * p.N];
-            }
-        }
+        const int rows = min(cnt - own, 8 * NB);             // of this warp's tokens (may be <= 0)
+        if (!GATED && p.residual) stage_residual<VEC>(p, token, rows, cnt_next, lane, mine);
         tmem_ld_wait();
-        __syncwarp();
-        const uint32_t row = (uint32_t)(lane & 7), blk = (uint32_t)(lane >> 3);   // fragment addresses: row, output block
-        const uint32_t frag = smem_u32(stage) + row * 64u + ((blk ^ ((row >> 1) & 3u)) << 4);
-        float z[32];
+        float z[32];                                          // [8 i + 2 b + h]: token 8 i + 2 (l % 4) + h, output block b
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {                       // 8 tokens
+        for (int i = 0; i < 4; ++i) {
             float2 sx = make_float2(1.0f, 1.0f);
             if (F8) {
                 const int tok = 8 * i + 2 * (lane & 3);
@@ -653,51 +660,87 @@ struct LinearWarp {
                 if (tok + 1 < cnt) sx.y = __ldg(p.sx + token + tok + 1);
             }
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {                   // 8 outputs
+            for (int b = 0; b < 4; ++b)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float a = __uint_as_float(v[16 * (b >> 1) + 4 * i + 2 * (b & 1) + h]);
                     if (F8) a *= (h ? sx.y : sx.x) * sw[b];
                     z[8 * i + 2 * b + h] = a + bias[b];
                 }
-            }
         }
-        linear_acts(p.act, z);
-        uint32_t out[4][4];
+        float o[8 * NB];
+        if (GATED) {
+            // the partner's 16 tokens go to it, this warp's come from it
+            float4* out = reinterpret_cast<float4*>(other) + lane;
+            const float4* in = reinterpret_cast<const float4*>(mine) + lane;
+            const bool up = own != 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+            for (int j = 0; j < 4; ++j) {
+                float4 w;
+                w.x = up ? z[4 * j] : z[16 + 4 * j];
+                w.y = up ? z[4 * j + 1] : z[16 + 4 * j + 1];
+                w.z = up ? z[4 * j + 2] : z[16 + 4 * j + 2];
+                w.w = up ? z[4 * j + 3] : z[16 + 4 * j + 3];
+                out[32 * j] = w;
+            }
+            named_barrier(bar, 64);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 w = in[32 * j];
+                const float r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float m = up ? z[16 + 4 * j + e] : z[4 * j + e];
+                    o[4 * j + e] = swiglu_f32(up ? r[e] : m, up ? m : r[e]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8 * NB; ++j) o[j] = z[j];
+            linear_acts(p.act, o);
+        }
+        __syncwarp();                                         // GATED: `mine` has been read
+        if (p.residual) {
+            if (GATED) stage_residual<VEC>(p, token, rows, cnt_next, lane, mine);
+            __syncwarp();
+        }
+        const uint32_t row = (uint32_t)(lane & 7), blk = (uint32_t)(lane >> 3);   // fragment addresses: row, output block
+        const uint32_t frag = smem_u32(mine) + row * 64u + ((blk ^ ((row >> 1) & 3u)) << 4);
+        uint32_t pk[NB][4];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
             uint32_t r4[4] = {0u, 0u, 0u, 0u};
             if (p.residual) ldmatrix_x4_trans(frag + (uint32_t)i * 512u, r4);
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                float lo = z[8 * i + 2 * b], hi = z[8 * i + 2 * b + 1];
+                float lo = o[8 * i + 2 * b], hi = o[8 * i + 2 * b + 1];
                 if (p.residual) {
                     lo += __uint_as_float(r4[b] << 16);
                     hi += __uint_as_float(r4[b] & 0xffff0000u);
                 }
-                out[i][b] = pack_bf16x2(lo, hi);
+                pk[i][b] = pack_bf16x2(lo, hi);
             }
         }
-        __syncwarp();                                       // the residual (or the last chunk's rows) has been read
+        __syncwarp();                                         // the residual has been read
 #pragma unroll
-        for (int i = 0; i < 4; ++i) stmatrix_x4_trans(frag + (uint32_t)i * 512u, out[i]);
+        for (int i = 0; i < NB; ++i) stmatrix_x4_trans(frag + (uint32_t)i * 512u, pk[i]);
         __syncwarp();
-        if (vec) {
+        if (VEC) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < NB; ++j) {
                 const int r = 8 * j + (lane >> 2);
-                const uint4 w = reinterpret_cast<const uint4*>(stage)[r * 4 + (q ^ ((r >> 1) & 3))];
-                if (r < cnt && 8 * q < nvalid) *reinterpret_cast<uint4*>(p.y + (token + r) * p.N + n + 8 * q) = w;
+                const uint4 w = reinterpret_cast<const uint4*>(mine)[r * 4 + (q ^ ((r >> 1) & 3))];
+                if (r < rows && 8 * q < nvalid)
+                    *reinterpret_cast<uint4*>(p.y + (token + own + r) * p.N + n + 8 * q) = w;
             }
         } else {
-            unsigned short* dst = reinterpret_cast<unsigned short*>(p.y) + token * p.N + n + lane;
-#pragma unroll 8
-            for (int r = 0; r < 32; ++r)
-                if (r < cnt && lane < nvalid)
+            unsigned short* dst = reinterpret_cast<unsigned short*>(p.y) + (token + own) * p.N + n + lane;
+#pragma unroll
+            for (int r = 0; r < 8 * NB; ++r)
+                if (r < rows && lane < nvalid)
                     dst[(long long)r * p.N] = reinterpret_cast<const unsigned short*>(
-                        stage)[r * 32 + (((lane >> 3) ^ ((r >> 1) & 3)) << 3) + (lane & 7)];
+                        mine)[r * 32 + (((lane >> 3) ^ ((r >> 1) & 3)) << 3) + (lane & 7)];
         }
-        __syncwarp();
     }
 };
 
@@ -710,8 +753,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sW = smem;
     uint8_t* sX = smem + LINP_STAGES * LIN_A_BYTES;
-    float* chunk = reinterpret_cast<float*>(smem + LINP_STAGES * LINP_STAGE_BYTES);
-    uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + LINP_STAGES * LINP_STAGE_BYTES + 2 * LINP_CHUNK_BYTES);
+    uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + LINP_STAGES * LINP_STAGE_BYTES + LINP_EPI_BYTES);
     uint64_t* empty_bar = full_bar + LINP_STAGES;
     uint64_t* tfull_bar = empty_bar + LINP_STAGES;
     uint64_t* tempty_bar = tfull_bar + 2;
@@ -828,84 +870,49 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             }
         }
     } else {
-        const int sub = warp & 3, half = (warp - 2) >> 2;           // lane quarter; half of a chunk's columns
+        // each of the two warps of a lane quarter takes half of the tokens; GATED: quarters q and q + 2 are partners
+        const int sub = warp & 3, half = (warp - 2) >> 2;
+        const int part = GATED ? sub & 1 : sub;                     // 32 outputs of the CTA
+        const bool up = GATED && sub >= 2;
+        const int bar = 1 + part + 2 * half;                        // GATED: the pair's barrier
         const int tid = threadIdx.x - 64;
+        uint8_t* rows = reinterpret_cast<uint8_t*>(smem + LINP_STAGES * LINP_STAGE_BYTES);
+        uint8_t* mine = rows + (sub + 4 * half) * 2048;             // 2 KB; the second set 16 KB further on
+        uint8_t* other = rows + ((sub ^ 2) + 4 * half) * 2048;
         const uint32_t tempty_leader = map_to_cta(tempty_bar, 0);
-        int acc = 0, buf = 0;
-        uint32_t acc_phase = 0;
-        const bool vec = (p.N & 3) == 0;
+        int acc = 0;
+        uint32_t acc_phase = 0, turn = 0;
         for (int t = pair; t < total; t += npairs) {
             const LinearTile ti = linear_tile(p, t, nt);
             const int n0 = (ti.n_idx * 2 + rank) * FT, nout = min(FT, p.N - n0);
-            if (!GATED) {
-                // each of the two warps of a lane quarter takes half of the tokens
-                const int c0 = half * 128, c1 = min(c0 + 128, ti.ntok);
-                LinearWarp<F8> e;
-                e.begin(p, n0 + sub * 32, lane);
-                e.stage = reinterpret_cast<uint8_t*>(chunk) + (warp - 2) * 2048;
-                if (p.residual && e.vec && c0 < c1) e.load_residual(p, ti.t0 + c0, min(32, c1 - c0), lane);
-                if (p.residual && nout > 0) {
-                    for (int i = tid; i < ti.ntok * 3; i += 256) {   // a row's piece is at most 3 lines
-                        const int tok = i / 3, col = min((i - tok * 3) * 64, nout - 1);
-                        prefetch_l2(p.residual + (long long)(ti.t0 + tok) * p.N + n0 + col);
-                    }
+            const int c0 = half * 128, c1 = min(c0 + 128, ti.ntok);
+            LinearWarp<F8, GATED> e;
+            e.begin(p, n0 + part * 32, up, lane);
+            if (p.residual && e.vec && c0 < c1) e.load_residual(p, ti.t0 + c0, c1 - c0, lane);
+            if (p.residual && nout > 0) {
+                for (int i = tid; i < ti.ntok * 3; i += 256) {       // a row's piece is at most 3 lines
+                    const int tok = i / 3, col = min((i - tok * 3) * 64, nout - 1);
+                    prefetch_l2(p.residual + (long long)(ti.t0 + tok) * p.N + n0 + col);
                 }
-                const bool ready = mbar_wait(tfull_bar + acc, acc_phase, abort_flag);
-                if (!__all_sync(0xffffffffu, ready)) break;
-                tc_fence_after();
-                const uint32_t tb = tmem_base + (uint32_t)(acc * GEMM_ACC_COLS) + ((uint32_t)(sub * 32) << 16);
-                for (int c = c0; c < c1; c += 32)
-                    e.chunk(p, tb + c, ti.t0 + c, min(32, c1 - c), min(32, c1 - c - 32), lane);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + (uint32_t)acc * 8u);
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1u;
-                continue;
             }
-            LinearCols<F8, GATED> cols;
-            uint2 ra[2], rb[2];
-            const int tk = tid >> 4;
-            if (vec) {
-                cols.load(p, tid, n0, nout);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    cols.residual(p, ti.t0 + min(tk + 16 * i, ti.ntok - 1), ra[i], rb[i]);
-            }
-            const bool ready = mbar_wait(tfull_bar + acc, acc_phase, abort_flag);
-            __syncwarp();
-            if (!named_barrier_all(1, 256, ready)) break;           // all eight warps go on, or none
+            bool ready = mbar_wait(tfull_bar + acc, acc_phase, abort_flag);
+            if (GATED) ready = named_barrier_all(bar, 64, ready);    // both partners go on, or neither
+            if (!__all_sync(0xffffffffu, ready)) break;
             tc_fence_after();
-            const uint32_t tbase = tmem_base + (uint32_t)(acc * GEMM_ACC_COLS) + ((uint32_t)(sub * 32) << 16) + half * 16;
-            for (int c = 0; c < ti.ntok; c += LINP_CHUNK) {
-                uint32_t v[16];
-                __syncwarp();
-                tmem_ld_16cols(tbase + c, v);
-                tmem_ld_wait();
-                float* dst = chunk + buf * (LINP_CHUNK * LIN_BM);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) dst[(half * 16 + j) * LIN_BM + sub * 32 + lane] = __uint_as_float(v[j]);
-                if (c + LINP_CHUNK >= ti.ntok) {                    // the accumulator has been read
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + (uint32_t)acc * 8u);
-                }
-                named_barrier(1, 256);                              // the chunk is staged
-                if (vec) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int tok = c + tk + 16 * i;
-                        const uint2 xa = ra[i], xb = rb[i];
-                        if (c + LINP_CHUNK < ti.ntok)
-                            cols.residual(p, ti.t0 + min(tok + LINP_CHUNK, ti.ntok - 1), ra[i], rb[i]);
-                        if (tok < ti.ntok)
-                            cols.template finish<1>(p, dst + (tk + 16 * i) * LIN_BM, 0, ti.t0 + tok, xa, xb);
-                    }
-                } else {
-                    linear_join<F8, GATED, 1>(p, dst, LINP_CHUNK, ti.t0 + c, min(LINP_CHUNK, ti.ntok - c), n0, nout, tid);
-                }
-                buf ^= 1;
+            const uint32_t tb = tmem_base + (uint32_t)(acc * GEMM_ACC_COLS) + ((uint32_t)(sub * 32) << 16);
+            for (int c = c0; c < c1; c += 32) {
+                const uint32_t set = (turn & 1u) * 16384u;
+                if (e.vec)
+                    e.template chunk<true>(p, tb + c, ti.t0 + c, min(32, c1 - c), c1 - c - 32, lane, mine + set,
+                                           other + set, bar);
+                else
+                    e.template chunk<false>(p, tb + c, ti.t0 + c, min(32, c1 - c), c1 - c - 32, lane, mine + set,
+                                            other + set, bar);
+                ++turn;
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + (uint32_t)acc * 8u);
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
