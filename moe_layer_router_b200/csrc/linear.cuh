@@ -57,15 +57,36 @@ __host__ __device__ constexpr int linear_smem_bytes(int stages, int bn, int own_
     return stages * (LIN_A_BYTES + bn * 128) + own_part_bytes + 1024 + 256;
 }
 
-// Activation of a pre-activation z (not SwiGLU).  gelu: z times the normal distribution function,
-// through erfc so that its tail keeps its relative precision; gelu_tanh: (1 + tanh u) / 2 =
-// sigmoid(2u) for the same reason.  The fast exponential and divide are a few ulp of fp32 off, far
-// below the bf16 rounding that follows.  relu keeps NaN.
+// Phi(-|z|) of the normal distribution: erfc(u) / 2 with u = |z| / sqrt(2) as t P(t) e^(-u^2) / 2, t = 1 / (1 + 0.4 u).
+// P is the degree-8 polynomial of least relative error against e^(u^2) erfc(u) / t on 0 < t <= 1 (1.3e-7, found by a
+// weighted least-squares iteration), halved here: the tail keeps its relative precision, at 20 instructions
+// where the library's erfc takes about twice as many (1152 x 7680 x 896: 45 us with that).
+__device__ __forceinline__ float normal_tail(float z) {
+    const float u = fabsf(z) * 0.70710678118654752f;
+    const float t = __fdividef(1.0f, fmaf(0.4f, u, 1.0f));
+    float q = 0.5f * 0.05026210844516754f;
+    q = fmaf(q, t, 0.5f * -0.18290141224861145f);
+    q = fmaf(q, t, 0.5f * 0.16908535361289978f);
+    q = fmaf(q, t, 0.5f * -0.005607480648905039f);
+    q = fmaf(q, t, 0.5f * 0.14143140614032745f);
+    q = fmaf(q, t, 0.5f * 0.16854198276996613f);
+    q = fmaf(q, t, 0.5f * 0.20784269273281097f);
+    q = fmaf(q, t, 0.5f * 0.22566959261894226f);
+    q = fmaf(q, t, 0.5f * 0.22567586600780487f);
+    return q * t * __expf(-u * u);
+}
+
+// Activation of a pre-activation z (not SwiGLU).  gelu: z Phi(z); gelu_tanh: (1 + tanh v) / 2 = sigmoid(2v), so that
+// neither tail cancels.  The fast exponential and divide are a few ulp of fp32 off, far below the bf16 rounding
+// that follows.  relu keeps NaN.
 __device__ __forceinline__ float linear_act(int act, float z) {
     switch (act) {
         case LIN_RELU: return z < 0.0f ? 0.0f : z;
         case LIN_SILU: return __fdividef(z, 1.0f + __expf(-z));
-        case LIN_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+        case LIN_GELU: {
+            const float q = normal_tail(z);
+            return z < 0.0f ? z * q : fmaf(-z, q, z);
+        }
         case LIN_GELU_TANH: return __fdividef(z, 1.0f + __expf(-1.5957691216057308f * fmaf(0.044715f * z * z, z, z)));
         default: return z;
     }
