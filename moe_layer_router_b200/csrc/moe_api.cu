@@ -377,6 +377,41 @@ int run_topk(const float* logits, int nsplit, float* logits_out, const float* bi
     return launch_status();
 }
 
+// Launch attributes of the dense layer's and the scored router's kernels: cluster size and programmatic
+// stream serialization (their prologue overlaps the end of the kernel in front of them; see grid_wait()).
+struct LaunchAttrs {
+    cudaLaunchAttribute a[2];
+    LaunchAttrs(cudaLaunchConfig_t* cfg, unsigned grid, unsigned block, size_t smem, cudaStream_t s, int cluster) {
+        memset(cfg, 0, sizeof(*cfg));
+        cfg->gridDim = dim3(grid);
+        cfg->blockDim = dim3(block);
+        cfg->dynamicSmemBytes = smem;
+        cfg->stream = s;
+        a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        a[0].val.programmaticStreamSerializationAllowed = 1;
+        a[1].id = cudaLaunchAttributeClusterDimension;
+        a[1].val.clusterDim.x = cluster;
+        a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;
+        cfg->attrs = a;
+        cfg->numAttrs = cluster > 1 ? 2 : 1;
+    }
+};
+
+// Lets a kernel use BYTES of dynamic shared memory on this device (set once per kernel and device).
+template <auto Kernel, int BYTES = GEMM_SMEM_MAX>
+int opt_in_smem() {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    static bool attr_set[kMaxDevices] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!attr_set[dev]) {
+        if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        attr_set[dev] = true;
+    }
+    return MOE_OK;
+}
+
 int check_route_params(const moe_route_params* r, int E, int k) {
     if (!r || (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) ||
         (r->group_score != MOE_GROUP_MAX && r->group_score != MOE_GROUP_TOP2) ||
@@ -389,7 +424,7 @@ int check_route_params(const moe_route_params* r, int E, int k) {
 }
 
 // Scored selection on `logits`; nsplit, logits_out as for run_topk.
-int run_route_scored(const float* logits, int nsplit, float* logits_out, const float* bias,
+int run_route_scored(DeviceInfo* di, const float* logits, int nsplit, float* logits_out, const float* bias,
                      const moe_route_params& r, int T, int E, int k, int32_t* idx, float* w, cudaStream_t s) {
     RouteScored p;
     memset(&p, 0, sizeof(p));
@@ -408,9 +443,46 @@ int run_route_scored(const float* logits, int nsplit, float* logits_out, const f
     p.by_logit = !bias && (r.n_group == 1 || !p.top2);
     p.idx = idx;
     p.w = w;
-    const int warps = route_f64_warps(E);
-    route_scored_f64_kernel<<<(unsigned)(((long long)T + warps - 1) / warps), warps * 32, (size_t)warps * E * 8, s>>>(p);
-    return launch_status();
+    // lanes: the largest power of two per group, its experts spread evenly over them
+    RouteLanes m;
+    m.lpg = 1;
+    while (m.lpg * 2 * r.n_group <= 32) m.lpg *= 2;
+    const int each = E / r.n_group;
+    m.per = (each + m.lpg - 1) / m.lpg;
+    const int used = (each + m.per - 1) / m.per;              // lanes of a group that hold experts
+    const int kept = r.n_group > 1 ? r.topk_group : 1;
+    // the largest candidate blocks of which there are k; fewer than 32 experts need no threshold
+    m.sub = -1;
+    if (kept * each > 32)
+        for (int b = 0; (1 << b) <= m.lpg && kept * ((used + (1 << b) - 1) >> b) >= k; ++b) m.sub = b;
+    m.kw = 1;
+    while (m.kw < k) m.kw *= 2;
+    const bool vec = nsplit == 1 && m.per % 4 == 0 && each % 4 == 0;
+    const size_t smem = (size_t)ROUTE_WARPS * E * sizeof(double);
+    const unsigned grid = (unsigned)std::min<long long>(((long long)T + ROUTE_WARPS - 1) / ROUTE_WARPS, 4ll * di->sms);
+    cudaLaunchConfig_t cfg;
+    const LaunchAttrs attrs(&cfg, grid, ROUTE_WARPS * 32, smem, s, 1);
+    int rc = MOE_OK;
+    cudaError_t e = cudaSuccess;
+#define MOE_ROUTE(EPL, VEC)                                                                               \
+    do {                                                                                                  \
+        if ((rc = opt_in_smem<route_scored_kernel<EPL, VEC>, ROUTE_WARPS * 1024 * 8>()) == MOE_OK)                                \
+            e = cudaLaunchKernelEx(&cfg, route_scored_kernel<EPL, VEC>, p, m);                            \
+    } while (0)
+    if (m.per <= 1) MOE_ROUTE(1, false);
+    else if (m.per <= 2) MOE_ROUTE(2, false);
+    else if (m.per <= 4) { if (vec) MOE_ROUTE(4, true); else MOE_ROUTE(4, false); }
+    else if (m.per <= 8) { if (vec) MOE_ROUTE(8, true); else MOE_ROUTE(8, false); }
+    else if (m.per <= 16) { if (vec) MOE_ROUTE(16, true); else MOE_ROUTE(16, false); }
+    else if (m.per <= 32) MOE_ROUTE(32, false);
+    else MOE_ROUTE(64, false);
+#undef MOE_ROUTE
+    if (rc != MOE_OK) return rc;
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
 }
 
 int run_permute(DeviceInfo* di, const moe_bf16* x, const int32_t* idx, int T, int d, int E, int k, long long C,
@@ -964,13 +1036,13 @@ int moe_route_scored(const moe_bf16* x, const moe_bf16* Wg, const float* bias, c
         if (logits_out && logits_out != logits_in &&
             cudaMemcpyAsync(logits_out, logits_in, (size_t)T * E * 4, cudaMemcpyDeviceToDevice, s) != cudaSuccess)
             return MOE_ERR_CUDA;
-        return run_route_scored(logits_in, 1, nullptr, bias, *params, T, E, k, idx, w, s);
+        return run_route_scored(di, logits_in, 1, nullptr, bias, *params, T, E, k, idx, w, s);
     }
     float* dst = logits_out ? logits_out : static_cast<float*>(ws);
     float* part = ks > 1 ? reinterpret_cast<float*>(static_cast<char*>(ws) + own) : nullptr;
     if ((rc = run_router_gemm(di, x, Wg, T, d, E, dst, part, ks, s)) != MOE_OK) return rc;
-    return ks > 1 ? run_route_scored(part, ks, dst, bias, *params, T, E, k, idx, w, s)
-                  : run_route_scored(dst, 1, nullptr, bias, *params, T, E, k, idx, w, s);
+    return ks > 1 ? run_route_scored(di, part, ks, dst, bias, *params, T, E, k, idx, w, s)
+                  : run_route_scored(di, dst, 1, nullptr, bias, *params, T, E, k, idx, w, s);
 }
 
 int moe_permute(const moe_bf16* x, const int32_t* idx, int T, int d, int E, int k, int64_t capacity,
@@ -1129,7 +1201,7 @@ int layer_phases(int phases, const moe_bf16* x, const moe_bf16* Wg, const float*
         if (!mark(ev.topk)) return MOE_ERR_CUDA;
         const float* lg = ks > 1 ? part : logits;
         float* sums = ks > 1 ? logits : nullptr;
-        rc = scored ? run_route_scored(lg, ks, sums, bias, *scored, T, E, k, idx, w, s)
+        rc = scored ? run_route_scored(di, lg, ks, sums, bias, *scored, T, E, k, idx, w, s)
                     : run_topk(lg, ks, sums, bias, T, E, k, idx, w, s);
         if (rc != MOE_OK) return rc;
     }
@@ -1256,26 +1328,6 @@ int check_linear(const void* x, const void* W, const void* W_up, const float* s,
     return MOE_OK;
 }
 
-// Launch attributes of the dense layer's and the scored router's kernels: cluster size and programmatic
-// stream serialization (their prologue overlaps the end of the kernel in front of them; see grid_wait()).
-struct LaunchAttrs {
-    cudaLaunchAttribute a[2];
-    LaunchAttrs(cudaLaunchConfig_t* cfg, unsigned grid, unsigned block, size_t smem, cudaStream_t s, int cluster) {
-        memset(cfg, 0, sizeof(*cfg));
-        cfg->gridDim = dim3(grid);
-        cfg->blockDim = dim3(block);
-        cfg->dynamicSmemBytes = smem;
-        cfg->stream = s;
-        a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        a[0].val.programmaticStreamSerializationAllowed = 1;
-        a[1].id = cudaLaunchAttributeClusterDimension;
-        a[1].val.clusterDim.x = cluster;
-        a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;
-        cfg->attrs = a;
-        cfg->numAttrs = cluster > 1 ? 2 : 1;
-    }
-};
-
 LinearParams linear_params(const LinearArgs& a) {
     LinearParams p;
     memset(&p, 0, sizeof(p));
@@ -1301,21 +1353,6 @@ int linear_maps(const LinearArgs& a, int x_rows, CUtensorMap* mW, CUtensorMap* m
         *mWup = *mW;
     }
     return mk(mX, a.x, a.M, x_rows);
-}
-
-// Lets a kernel use the whole opt-in shared memory on this device (once per kernel and device).
-template <auto Kernel>
-int linear_smem_attr() {
-    std::lock_guard<std::mutex> lock(g_mutex);
-    static bool attr_set[kMaxDevices] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (!attr_set[dev]) {
-        if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM_MAX) != cudaSuccess)
-            return MOE_ERR_CUDA;
-        attr_set[dev] = true;
-    }
-    return MOE_OK;
 }
 
 // Tiles of linear_split_kernel.  Token tiles: one up to 128 tokens, then tiles of about 128; short K (up to
@@ -1345,7 +1382,7 @@ int launch_linear_split(const LinearArgs& a, cudaStream_t s) {
     CUtensorMap mW, mWup, mX;
     int rc = linear_maps<F8, GATED>(a, p.bn, &mW, &mWup, &mX);
     if (rc != MOE_OK) return rc;
-    if ((rc = linear_smem_attr<linear_split_kernel<F8, GATED>>()) != MOE_OK) return rc;
+    if ((rc = opt_in_smem<linear_split_kernel<F8, GATED>>()) != MOE_OK) return rc;
     cudaLaunchConfig_t cfg;
     const LaunchAttrs attrs(&cfg, (unsigned)(tiles * p.split), LIN_THREADS,
                             linear_smem_bytes(p.stages, p.bn, p.own_part ? linear_part_bytes(p.bn, p.split) : 0), s,
@@ -1380,7 +1417,7 @@ int launch_linear_pair(DeviceInfo* di, const LinearArgs& a, cudaStream_t s) {
     CUtensorMap mW, mWup, mX;
     int rc = linear_maps<F8, GATED>(a, p.bn / 2, &mW, &mWup, &mX);
     if (rc != MOE_OK) return rc;
-    if ((rc = linear_smem_attr<linear_pair_kernel<F8, GATED>>()) != MOE_OK) return rc;
+    if ((rc = opt_in_smem<linear_pair_kernel<F8, GATED>>()) != MOE_OK) return rc;
     cudaLaunchConfig_t cfg;
     const LaunchAttrs attrs(&cfg, 2 * (unsigned)std::min(tiles, pairs), LINP_THREADS, LINP_SMEM_BYTES, s, 1);
     if (cudaLaunchKernelEx(&cfg, linear_pair_kernel<F8, GATED>, mW, mWup, mX, p) != cudaSuccess) {
