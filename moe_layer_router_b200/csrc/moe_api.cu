@@ -445,37 +445,36 @@ int run_route_scored(DeviceInfo* di, const float* logits, int nsplit, float* log
     p.w = w;
     // lanes: the largest power of two per group, its experts spread evenly over them
     RouteLanes m;
-    m.lpg = 1;
-    while (m.lpg * 2 * r.n_group <= 32) m.lpg *= 2;
+    m.lg = 0;
+    while ((2 << m.lg) * r.n_group <= 32) ++m.lg;
     const int each = E / r.n_group;
-    m.per = (each + m.lpg - 1) / m.lpg;
-    const int used = (each + m.per - 1) / m.per;              // lanes of a group that hold experts
-    const int kept = r.n_group > 1 ? r.topk_group : 1;
-    // the largest candidate blocks of which there are k; fewer than 32 experts need no threshold
-    m.sub = -1;
-    if (kept * each > 32)
-        for (int b = 0; (1 << b) <= m.lpg && kept * ((used + (1 << b) - 1) >> b) >= k; ++b) m.sub = b;
-    m.kw = 1;
-    while (m.kw < k) m.kw *= 2;
+    m.per = (each + (1 << m.lg) - 1) >> m.lg;
+    m.each = each;
     const bool vec = nsplit == 1 && m.per % 4 == 0 && each % 4 == 0;
-    const size_t smem = (size_t)ROUTE_WARPS * E * sizeof(double);
+    const size_t smem = (size_t)ROUTE_WARPS * 32 * m.per * sizeof(double);
     const unsigned grid = (unsigned)std::min<long long>(((long long)T + ROUTE_WARPS - 1) / ROUTE_WARPS, 4ll * di->sms);
+    const int kind = p.by_logit ? ROUTE_LOGIT : p.sigmoid ? ROUTE_SIGMOID : ROUTE_SOFTMAX;
     cudaLaunchConfig_t cfg;
     const LaunchAttrs attrs(&cfg, grid, ROUTE_WARPS * 32, smem, s, 1);
     int rc = MOE_OK;
     cudaError_t e = cudaSuccess;
-#define MOE_ROUTE(EPL, VEC)                                                                               \
-    do {                                                                                                  \
-        if ((rc = opt_in_smem<route_scored_kernel<EPL, VEC>, ROUTE_WARPS * 1024 * 8>()) == MOE_OK)                                \
-            e = cudaLaunchKernelEx(&cfg, route_scored_kernel<EPL, VEC>, p, m);                            \
+#define MOE_ROUTE_KIND(EPL, VEC, KIND)                                                                            \
+    if ((rc = opt_in_smem<route_scored_kernel<EPL, VEC, KIND>, ROUTE_WARPS * 32 * EPL * 8>()) == MOE_OK)          \
+        e = cudaLaunchKernelEx(&cfg, route_scored_kernel<EPL, VEC, KIND>, p, m);
+#define MOE_ROUTE(EPL, VEC)                                                                                       \
+    do {                                                                                                          \
+        if (kind == ROUTE_LOGIT) { MOE_ROUTE_KIND(EPL, VEC, ROUTE_LOGIT) }                                        \
+        else if (kind == ROUTE_SIGMOID) { MOE_ROUTE_KIND(EPL, VEC, ROUTE_SIGMOID) }                               \
+        else { MOE_ROUTE_KIND(EPL, VEC, ROUTE_SOFTMAX) }                                                          \
     } while (0)
     if (m.per <= 1) MOE_ROUTE(1, false);
     else if (m.per <= 2) MOE_ROUTE(2, false);
     else if (m.per <= 4) { if (vec) MOE_ROUTE(4, true); else MOE_ROUTE(4, false); }
     else if (m.per <= 8) { if (vec) MOE_ROUTE(8, true); else MOE_ROUTE(8, false); }
-    else if (m.per <= 16) { if (vec) MOE_ROUTE(16, true); else MOE_ROUTE(16, false); }
+    else if (m.per <= 16) MOE_ROUTE(16, false);
     else if (m.per <= 32) MOE_ROUTE(32, false);
     else MOE_ROUTE(64, false);
+#undef MOE_ROUTE_KIND
 #undef MOE_ROUTE
     if (rc != MOE_OK) return rc;
     if (e != cudaSuccess) {

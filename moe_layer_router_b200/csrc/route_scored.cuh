@@ -44,35 +44,53 @@ __device__ __forceinline__ float scored_logit(const RouteScored& p, const float*
     return l;
 }
 
-// key order in 64 bits: larger first, equal keys -> lower expert
-__device__ __forceinline__ bool key64_before(double ka, int ea, double kb, int eb) {
-    return ka > kb || (ka == kb && ea < eb);
+// floats as integers of the same order (no NaN; -0 must have been made +0)
+__device__ __forceinline__ int ordered(float f) {
+    const int b = __float_as_int(f);
+    return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+constexpr int ORD_LOWEST = (int)0x80800000;    // ordered(-FLT_MAX): every unmasked key is at least this
+constexpr int ORD_EMPTY = (int)0x80000000;
+
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// e^x, subnormal results as 0
+__device__ __forceinline__ float exp_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
 }
 
 // The weights of the selected experts: lane j < k holds slot j's expert (-1: none) and logit.
 // top / total: the row's largest logit and sum of e^(l - top) over its unmasked experts (softmax
 // without renormalisation).  Renormalised weights are ratios of scores, taken relative to the largest
-// selected one so that scores that underflow still have their ratio:
-//   softmax  s_j ~ e^(l_j - m),  sigmoid  s_j = e^l_j / (1 + e^l_j) ~ e^(l_j - m) / (1 + e^l_j)
-// with m the largest selected logit (sigmoid: at most 0).  Warp-collective.
-// kw: a power of two >= k, the lanes that the sums run over.
+// selected one where they would underflow: s_j ~ e^(l_j - m) in softmax, and in sigmoid once all selected
+// logits are below -60.  Warp-collective.
 __device__ __forceinline__ void scored_weights(const RouteScored& p, long long t, int lane, int my_e, float my_l,
-                                               float top, float total, int kw) {
+                                               float top, float total) {
     const bool have = lane < p.k && my_e >= 0;
     float s = 0.0f;
-    if (p.renorm) {
-        float m = have ? my_l : -INFINITY;
-        for (int o = kw >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (p.sigmoid) m = fminf(m, 0.0f);
-        if (have) {
-            if (!p.sigmoid) s = expf(my_l - m);
-            else s = my_l >= 0.0f ? 1.0f / (1.0f + expf(-my_l)) : expf(my_l - m) / (1.0f + expf(my_l));
+    if (!p.sigmoid) {
+        if (p.renorm) {      // as moe_route computes them: the same weights, bit for bit
+            const float m = from_ordered(__reduce_max_sync(0xffffffffu, ordered((have ? my_l : -INFINITY) + 0.0f)));
+            if (have) s = expf(my_l - m);
+            s /= warp_sum(s);
+        } else if (have) {
+            s = expf(my_l - top) / total;
         }
-        float sum = s;
-        for (int o = kw >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (have) s /= sum;
-    } else if (have) {
-        s = p.sigmoid ? 1.0f / (1.0f + expf(-my_l)) : expf(my_l - top) / total;
+    } else {
+        if (have) s = rcp_approx(1.0f + exp_approx(-my_l));   // a few ulp
+        if (p.renorm) {
+            if (!__any_sync(0xffffffffu, have && my_l > -60.0f)) {
+                const float m = from_ordered(__reduce_max_sync(0xffffffffu, ordered(have ? my_l : -INFINITY)));
+                if (have) s = expf(my_l - m);                 // 1 + e^l is 1
+            }
+            s *= rcp_approx(warp_sum(s));
+        }
     }
     if (lane < p.k) {
         p.idx[t * p.k + lane] = have ? my_e : -1;
@@ -80,100 +98,125 @@ __device__ __forceinline__ void scored_weights(const RouteScored& p, long long t
     }
 }
 
-// One token by one warp with every key in 64 bits, in the caller's shared memory (E doubles).
-// bad: set when a logit or bias is NaN or +inf (that expert is masked).
-__device__ __noinline__ void route_token_f64(const RouteScored& p, long long t, int lane, double* keys) {
-    const float* row = p.logits + t * p.E;
-    bool bad = false;
-    float top = -INFINITY;
-    auto usable = [&](float l, float b) { return l < INFINITY && l > -INFINITY && b < INFINITY && b > -INFINITY; };
-    for (int e = lane; e < p.E; e += 32) {
-        const float l = scored_logit(p, row, e), b = p.bias ? __ldg(p.bias + e) : 0.0f;
-        bad |= !(l < INFINITY) || !(b < INFINITY);
-        if (l < INFINITY) top = fmaxf(top, l);
-        if (p.nsplit > 1 && p.logits_out) p.logits_out[t * p.E + e] = l;
+// Experts of a warp's lanes: group g on 2^lg lanes, each holding up to `per` consecutive experts (the last lanes of
+// a group fewer), so that (lane, position) is the order of the experts.
+struct RouteLanes {
+    int lg, per;
+    int each;     // E / n_group
+};
+struct RouteLane {
+    int group, e0, cnt;
+    __device__ __forceinline__ RouteLane(const RouteScored& p, const RouteLanes& m, int lane) {
+        const int part = lane & ((1 << m.lg) - 1);
+        group = lane >> m.lg;
+        e0 = group * m.each + part * m.per;
+        cnt = group < p.n_group ? max(0, min(m.per, m.each - part * m.per)) : 0;
     }
-    if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(-7 /* MOE_ERR_CHECK */);
-    top = warp_max(top);
+};
+
+// doubles as integers of the same order (no NaN, no -0)
+__device__ __forceinline__ long long ordered64(double d) {
+    const long long b = __double_as_longlong(d);
+    return b ^ ((b >> 63) & 0x7fffffffffffffffll);
+}
+
+// One token by one warp with every key in 64 bits, in the caller's shared memory (32 `per` doubles, expert i of
+// lane q at [32 i + q]).  Experts whose logit or bias is NaN or +inf are masked (the caller has reported them).
+__device__ __noinline__ void route_token_f64(const RouteScored& p, const RouteLanes& m, long long t, int lane,
+                                             double* keys) {
+    const unsigned all = 0xffffffffu;
+    const float* row = p.logits + t * p.E;
+    const RouteLane at(p, m, lane);
+    float top = -INFINITY;
     double total = 0.0;
     if (!p.sigmoid) {
-        for (int e = lane; e < p.E; e += 32) {
-            const float l = scored_logit(p, row, e);
-            if (l < INFINITY && l > -INFINITY) total += exp((double)l - (double)top);
+        for (int i = 0; i < at.cnt; ++i) {
+            const float l = scored_logit(p, row, at.e0 + i);
+            if (l < INFINITY) top = fmaxf(top, l);
+        }
+        top = warp_max(top);
+#pragma unroll 4
+        for (int i = 0; i < at.cnt; ++i) {
+            const float l = scored_logit(p, row, at.e0 + i);
+            total += l < INFINITY && l > -INFINITY ? exp((double)l - (double)top) : 0.0;
         }
         total = warp_sum(total);
     }
-    for (int e = lane; e < p.E; e += 32) {
-        const float l = scored_logit(p, row, e), b = p.bias ? __ldg(p.bias + e) : 0.0f;
-        double key = -INFINITY;
-        if (usable(l, b)) {
-            if (p.by_logit) key = l;
-            else key = (p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top) / total) + (double)b;
+    double a = -INFINITY, b = -INFINITY;          // the lane's two largest keys
+    int best = 0;                                 // position of a
+#pragma unroll 4
+    for (int i = 0; i < at.cnt; ++i) {
+        const float l = scored_logit(p, row, at.e0 + i), bias = p.bias ? __ldg(p.bias + at.e0 + i) : 0.0f;
+        double key = l;
+        if (!p.by_logit)
+            key = (p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top) / total) + (double)bias;
+        if (!(l < INFINITY && l > -INFINITY && bias < INFINITY && bias > -INFINITY)) key = -INFINITY;
+        key += 0.0;                               // -0 -> +0
+        keys[32 * i + lane] = key;
+        if (key > a) {
+            b = a;
+            a = key;
+            best = i;
+        } else if (key > b) {
+            b = key;
         }
-        keys[e] = key;
     }
-    __syncwarp();
     if (p.n_group > 1) {
-        // lane g: the value of group g, then its rank among all
-        const int each = p.E / p.n_group;
-        double v = -INFINITY;
-        if (lane < p.n_group) {
-            double a = -INFINITY, b = -INFINITY;
-            for (int i = 0; i < each; ++i) {
-                const double x = keys[lane * each + i];
-                if (x > a) { b = a; a = x; } else if (x > b) { b = x; }
-            }
-            v = p.top2 && b > -INFINITY ? a + b : a;
+        double v = a, w = b;
+        for (int o = 1; o < (1 << m.lg); o <<= 1) {
+            const double v2 = __shfl_xor_sync(all, v, o), w2 = __shfl_xor_sync(all, w, o);
+            w = fmax(fmax(w, w2), fmin(v, v2));
+            v = fmax(v, v2);
         }
+        if (p.top2 && w > -INFINITY) v += w;
         int rank = 0;
-        for (int g = 0; g < p.n_group; ++g) {
-            const double o = __shfl_sync(0xffffffffu, v, g);
-            rank += key64_before(o, g, v, lane);
+        for (int q = 0; q < p.n_group; ++q) {
+            const double o = __shfl_sync(all, v, q << m.lg);
+            rank += o > v || (o == v && q < at.group);
         }
-        const uint32_t kept = __ballot_sync(0xffffffffu, lane < p.n_group && rank < p.topk_group);
-        __syncwarp();
-        for (int e = lane; e < p.E; e += 32)
-            if (!((kept >> (e / each)) & 1u)) keys[e] = -INFINITY;
-        __syncwarp();
+        if (at.group >= p.n_group || rank >= p.topk_group) a = -INFINITY;
     }
     int my_e = -1;
     for (int j = 0; j < p.k; ++j) {
-        double bk = -INFINITY;
-        int be = 0x7fffffff;
-        for (int e = lane; e < p.E; e += 32)
-            if (keys[e] > bk) { bk = keys[e]; be = e; }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const double ok = __shfl_xor_sync(0xffffffffu, bk, o);
-            const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-            if (key64_before(ok, oe, bk, be)) { bk = ok; be = oe; }
+        // the largest head, the lowest lane of equal ones
+        const long long o = ordered64(a);
+        const int hi = (int)(o >> 32);
+        const bool first = hi == __reduce_max_sync(all, hi);
+        const unsigned lo = (unsigned)o;
+        const unsigned most = __reduce_max_sync(all, first ? lo : 0u);
+        const int owner = __ffs(__ballot_sync(all, first && lo == most)) - 1;
+        if (!(__shfl_sync(all, a, owner) > -INFINITY)) break;      // no unmasked expert left
+        const int e = __shfl_sync(all, at.e0 + best, owner);
+        if (lane == j) my_e = e;
+        if (lane == owner) {
+            keys[32 * best + lane] = -INFINITY;
+            a = -INFINITY;
+#pragma unroll 4
+            for (int i = 0; i < at.cnt; ++i) {
+                const double key = keys[32 * i + lane];
+                if (key > a) {
+                    a = key;
+                    best = i;
+                }
+            }
         }
-        if (be >= p.E) break;               // no unmasked expert left
-        if (lane == j) my_e = be;
-        __syncwarp();
-        if (lane == 0) keys[be] = -INFINITY;
-        __syncwarp();
     }
     const float my_l = my_e >= 0 ? scored_logit(p, row, my_e) : 0.0f;
-    scored_weights(p, t, lane, my_e, my_l, top, (float)total, 32);
+    scored_weights(p, t, lane, my_e, my_l, top, (float)total);
 }
 
 // ---------------------------------------------------------------- the kernel: keys in 32 bits
 //
-// One warp per token; group g of experts lies on LPG = 2^x <= 32 / n_group lanes, each holding up to EPL
-// consecutive experts, so that (lane, position) is the order of the experts.  Keys are kept as integers of the
-// same order.
-//   groups      two largest keys per lane, merged over the group's lanes; rank by n_group shuffles
-//   candidates  the lanes of the groups that stay form at least k blocks of 2^sub lanes; the smallest of the blocks'
-//               maxima is exceeded by at least k keys.  The keys not below it (less their error) are moved to shared
-//               memory, typically 2 k to 3 k of them, and each is ranked against all.  More than ROUTE_CAND: the k + 1
-//               largest are taken out one by one instead.
-//   certainty   32-bit keys are at most route_err off.  Where two neighbours in the order, or the last group that
-//               stays and the first that does not, are closer than that, the token is done again in 64 bits
-//               (route_token_f64): about one token in a thousand for scores of unit variance.
-//   weights     from the selected logits, with the library's expf
-// 32768 x 256, 8 groups, k = 8: the logits alone are 33.5 MB, 5.2 us at the measured copy rate.
-constexpr int ROUTE_CAND = 64;
+// One warp per token, its experts on the lanes as RouteLanes has them, EPL >= per.  Keys are integers of the floats' order whose
+// last BITS bits hold the position in the lane: a comparison carries the expert along and a lane's keys are distinct.
+//   lanes       sort their four largest keys (8 experts: 32 minima and maxima)
+//   groups      the two largest keys merged over the group's lanes; rank by n_group shuffles
+//   slots       k + 1 times: the warp's largest list head (one redux), taken off its lane's list; a lane whose four
+//               are used up sorts its next four
+//   certainty   keys are off by at most route_err and 2^BITS steps.  Where two neighbours in the order, or the last
+//               group that stays and the first that does not, are closer than that, the token is done again
+//               in 64 bits (route_token_f64): about one token in 500 for scores of unit variance, 256 experts
+// Bound by the instructions, not by the 33.5 MB of logits that 32768 x 256 has (5.2 us at the measured copy rate).
 constexpr int ROUTE_WARPS = 8;
 
 // Errors in units of 2^-23.  The fast exponential of x is off by at most 2 + 1.16 |x| of its value (x = -l, or
@@ -188,59 +231,81 @@ __device__ __forceinline__ float route_err(bool sigmoid, float s, float x, float
     return 1.1920929e-7f * fmaf(s, rel, fabsf(key)) + 1e-36f;
 }
 __device__ __forceinline__ float route_err_any(bool sigmoid, float key, float bmax) {
-    return sigmoid ? 4.8e-7f * (1.0f + fabsf(key)) : 1.7e-5f * (fabsf(key) + bmax) + 1e-17f;
+    return sigmoid ? 4.8e-7f * (1.0f + fabsf(key) + bmax) : 1.7e-5f * (fabsf(key) + 2.0f * bmax) + 1e-17f;
 }
 
-// floats as integers of the same order (no NaN; -0 must have been made +0)
-__device__ __forceinline__ int ordered(float f) {
-    const int b = __float_as_int(f);
-    return b ^ ((b >> 31) & 0x7fffffff);
+__device__ __forceinline__ void order2(int& a, int& b) {      // a >= b
+    const int hi = max(a, b);
+    b = min(a, b);
+    a = hi;
 }
-__device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
-constexpr int ORD_NONE = (int)0x807fffff;      // ordered(-inf): a masked expert
 
-struct RouteLanes {
-    int lpg;      // lanes per group
-    int per;      // experts per lane (the last lanes of a group may hold fewer)
-    int sub;      // log2 of the lanes of a candidate block; < 0: every key is a candidate
-    int kw;       // power of two >= k
-};
+// The D = min(EPL, 4) largest of key[] below `bound`, in descending order.
+template <int EPL, int D>
+__device__ __forceinline__ void largest(const int (&key)[EPL], int bound, int (&top)[D]) {
+    if (EPL < 4) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) top[i] = key[i] < bound ? key[i] : ORD_EMPTY;
+        if (D == 2) order2(top[0], top[D - 1]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < EPL; q += 4) {
+            int v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = key[(q + i) % EPL] < bound ? key[(q + i) % EPL] : ORD_EMPTY;
+            order2(v[0], v[1]); order2(v[2], v[3]); order2(v[0], v[2]); order2(v[1], v[3]); order2(v[1], v[2]);
+            if (q == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top[i % D] = v[i];
+            } else {      // the larger half of two sorted lists, then in order
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top[i % D] = max(top[i % D], v[3 - i]);
+                order2(top[0], top[2 % D]); order2(top[1 % D], top[3 % D]);
+                order2(top[0], top[1 % D]); order2(top[2 % D], top[3 % D]);
+            }
+        }
+    }
+}
 
-template <int EPL, bool VEC>
-__global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scored_kernel(const __grid_constant__ RouteScored p,
+enum { ROUTE_LOGIT = 0, ROUTE_SIGMOID = 1, ROUTE_SOFTMAX = 2 };   // what a key is
+
+template <int EPL, bool VEC, int KIND>
+__global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 4 : 1) route_scored_kernel(const __grid_constant__ RouteScored p,
                                                                         const __grid_constant__ RouteLanes m) {
-    extern __shared__ double route_keys[];      // route_token_f64: E doubles per warp
-    __shared__ __align__(16) int c_key[ROUTE_WARPS][ROUTE_CAND + 4];
-    __shared__ int c_idx[ROUTE_WARPS][ROUTE_CAND];
-    __shared__ float c_l[ROUTE_WARPS][ROUTE_CAND];
-    __shared__ int o_key[ROUTE_WARPS][MAX_TOPK + 1], o_idx[ROUTE_WARPS][MAX_TOPK + 1];
-    __shared__ float o_l[ROUTE_WARPS][MAX_TOPK + 1];
+    extern __shared__ double route_keys[];      // route_token_f64: 32 `per` doubles per warp
+    constexpr int BITS = EPL <= 1 ? 0 : EPL <= 2 ? 1 : EPL <= 4 ? 2 : EPL <= 8 ? 3 : EPL <= 16 ? 4 : EPL <= 32 ? 5 : 6;
+    constexpr int POS = (1 << BITS) - 1;
+    constexpr int D = EPL < 4 ? EPL : 4;
+    constexpr float TRUNC = 1.1920929e-7f * (1 << BITS);       // relative, of the position's bits
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned all = 0xffffffffu;
-    const int each = p.E / p.n_group;
-    const int g = lane / m.lpg, part = lane - g * m.lpg;
-    const int e0 = g * each + part * m.per;
-    const int cnt = g < p.n_group ? max(0, min(m.per, each - part * m.per)) : 0;
+    const RouteLane at(p, m, lane);
+    const int g = at.group, e0 = at.e0, cnt = at.cnt;
     constexpr bool KEEP_BIAS = EPL <= 8;
     float bias[KEEP_BIAS ? EPL : 1];
     grid_wait();
     grid_launch_next();
     float bmax = 0.0f;                           // of the finite biases
     if (p.bias) {
+        bool bad = false;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             const float b = i < cnt ? __ldg(p.bias + e0 + i) : 0.0f;
-            if (KEEP_BIAS) bias[KEEP_BIAS ? i : 0] = b;
+            if (KEEP_BIAS) bias[KEEP_BIAS ? i : 0] = b < INFINITY ? b : -INFINITY;
             if (fabsf(b) < INFINITY) bmax = fmaxf(bmax, fabsf(b));
+            bad |= !(b < INFINITY);
         }
         bmax = __int_as_float(__reduce_max_sync(all, __float_as_int(bmax)));
+        if (bad) record_error(-7 /* MOE_ERR_CHECK */);
     } else if (KEEP_BIAS) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) bias[KEEP_BIAS ? i : 0] = 0.0f;
     }
-    for (long long t = (long long)blockIdx.x * ROUTE_WARPS + warp; t < p.T; t += (long long)gridDim.x * ROUTE_WARPS) {
-        const float* row = p.logits + t * p.E;
-        float l[EPL];
+    const long long stride = (long long)gridDim.x * ROUTE_WARPS;
+    long long t = (long long)blockIdx.x * ROUTE_WARPS + warp;
+    float l[EPL];
+    auto load = [&](long long tok) {
+        const float* row = p.logits + tok * p.E;
         if (VEC) {
 #pragma unroll
             for (int i = 0; i < EPL; i += 4) {
@@ -259,196 +324,142 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_scored_kernel(const __
             if (p.nsplit > 1 && p.logits_out) {
 #pragma unroll
                 for (int i = 0; i < EPL; ++i)
-                    if (i < cnt) p.logits_out[t * p.E + e0 + i] = l[i];
+                    if (i < cnt) p.logits_out[tok * p.E + e0 + i] = l[i];
             }
         }
-        // ---- keys (ordered integers); masked experts ORD_NONE
+    };
+    if (t < p.T) load(t);
+    for (; t < p.T; t += stride) {
+        const float* row = p.logits + t * p.E;
+        // ---- keys
         bool bad = false;
-        float top = -INFINITY, total = 1.0f;
+        float top = -INFINITY, total = 1.0f, inv = 1.0f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            if (!(l[i] < INFINITY)) {
-                bad = true;
-                l[i] = -INFINITY;
-            }
-            if (!p.sigmoid) top = fmaxf(top, l[i]);
+            bad |= !(l[i] < INFINITY);
+            l[i] = l[i] < INFINITY ? l[i] : -INFINITY;
         }
-        int key[EPL];
-        if (!p.sigmoid && !(p.by_logit && p.renorm)) {
+        if (__any_sync(all, bad) && lane == 0) record_error(-7 /* MOE_ERR_CHECK */);
+        float ex[EPL];                                        // e^(l - top) or e^-l
+        if (KIND == ROUTE_SOFTMAX || (KIND == ROUTE_LOGIT && !p.sigmoid && !p.renorm)) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) top = fmaxf(top, l[i]);
             top = from_ordered(__reduce_max_sync(all, ordered(top + 0.0f)));
-            float part_sum = 0.0f;
             const float ref = top > -INFINITY ? top : 0.0f;
-            float ex[EPL];
+            float part_sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
-                ex[i] = __expf(l[i] - ref);                   // 0 for -inf
+                ex[i] = exp_approx(l[i] - ref);               // 0 for -inf
                 part_sum += ex[i];
             }
             total = warp_sum(part_sum);
-            const float inv = __fdividef(1.0f, total);
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const float b = KEEP_BIAS ? bias[KEEP_BIAS ? i : 0] : (p.bias && i < cnt ? __ldg(p.bias + e0 + i) : 0.0f);
-                bad |= !(b < INFINITY);
-                const float k32 = (p.by_logit ? l[i] : ex[i] * inv + b) + 0.0f;
-                key[i] = l[i] > -INFINITY && b > -INFINITY && b < INFINITY ? ordered(k32) : ORD_NONE;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const float b = KEEP_BIAS ? bias[KEEP_BIAS ? i : 0] : (p.bias && i < cnt ? __ldg(p.bias + e0 + i) : 0.0f);
-                bad |= !(b < INFINITY);
-                const float k32 = (p.by_logit ? l[i] : __fdividef(1.0f, 1.0f + __expf(-l[i])) + b) + 0.0f;
-                key[i] = l[i] > -INFINITY && b > -INFINITY && b < INFINITY ? ordered(k32) : ORD_NONE;
-            }
+            inv = 1.0f / total;
         }
-        if (__any_sync(all, bad) && lane == 0) record_error(-7 /* MOE_ERR_CHECK */);
+        int key[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            float k32 = l[i];
+            if (KIND != ROUTE_LOGIT) {
+                float b = 0.0f;
+                if (KEEP_BIAS) b = bias[KEEP_BIAS ? i : 0];
+                else if (p.bias && i < cnt) {
+                    b = __ldg(p.bias + e0 + i);
+                    b = b < INFINITY ? b : -INFINITY;
+                }
+                const float s = KIND == ROUTE_SIGMOID ? rcp_approx(1.0f + exp_approx(-l[i])) : ex[i] * inv;
+                k32 = l[i] > -INFINITY ? s + b : -INFINITY;
+            }
+            key[i] = (ordered(k32 + 0.0f) & ~POS) | (POS - i);
+        }
+        if (t + stride < p.T) load(t + stride);               // on its way while this token is finished
+        int head[D];
+        largest<EPL, D>(key, 0x7fffffff, head);
         bool sure = true;
         // ---- groups
         if (p.n_group > 1) {
-            int a = ORD_NONE, b = ORD_NONE;                   // two largest
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                b = max(b, min(a, key[i]));
-                a = max(a, key[i]);
-            }
-            for (int o = 1; o < m.lpg; o <<= 1) {
+            int a = head[0], b = D > 1 ? head[D > 1 ? 1 : 0] : ORD_EMPTY;
+            for (int o = 1; o < (1 << m.lg); o <<= 1) {
                 const int a2 = __shfl_xor_sync(all, a, o), b2 = __shfl_xor_sync(all, b, o);
                 b = max(max(b, b2), min(a, a2));
                 a = max(a, a2);
             }
-            if (p.top2 && b != ORD_NONE) a = max(ORD_NONE + 1, ordered(from_ordered(a) + from_ordered(b) + 0.0f));
-            int rank = 0;
-            for (int q = 0; q < p.n_group; ++q) {
-                const int o = __shfl_sync(all, a, q * m.lpg);
-                rank += o > a || (o == a && q < g);
-            }
-            const bool kept = g < p.n_group && rank < p.topk_group;
-            if (!p.by_logit) {
-                const int lo = __reduce_min_sync(all, kept ? a : 0x7fffffff);
-                const int hi = __reduce_max_sync(all, !kept && g < p.n_group ? a : ORD_NONE);
-                if (hi != ORD_NONE) {
-                    const float fl = from_ordered(lo), fh = from_ordered(hi);
-                    // a value is one key, or two: each within the error of a key of twice its size
-                    sure = fl - fh > 2.0f * (route_err_any(p.sigmoid, 2.0f * fl, bmax) + route_err_any(p.sigmoid, 2.0f * fh, bmax));
+            // the value as an ordered integer (without positions); EMPTY: no expert left
+            int v = a >= ORD_LOWEST ? a & ~POS : ORD_EMPTY;
+            if (p.top2 && b >= ORD_LOWEST)
+                v = max(ORD_LOWEST, ordered(from_ordered(a & ~POS) + from_ordered(b & ~POS) + 0.0f));
+            if (g >= p.n_group) v = ORD_EMPTY;
+            // the topk_group largest, one by one; lo: the last of them, hi: the largest left
+            bool kept = false;
+            int lo = ORD_EMPTY;
+            for (int q = 0; q < p.topk_group; ++q) {
+                const int most = __reduce_max_sync(all, v);
+                if (most == ORD_EMPTY) break;
+                lo = most;
+                const int owner = __ffs(__ballot_sync(all, v == most)) - 1;
+                if (g == (owner >> m.lg)) {
+                    kept = true;
+                    v = ORD_EMPTY;
                 }
+            }
+            const int hi = __reduce_max_sync(all, v);
+            if (hi != ORD_EMPTY) {
+                const float fl = from_ordered(lo), fh = from_ordered(hi);
+                // a value is one key, or two: each within the error of a key of twice its size
+                sure = KIND == ROUTE_LOGIT ? lo > hi
+                                           : fl - fh > 2.0f * (route_err_any(p.sigmoid, 2.0f * fl, bmax) +
+                                                               route_err_any(p.sigmoid, 2.0f * fh, bmax)) +
+                                                           4.0f * TRUNC * (fabsf(fl) + fabsf(fh) + bmax);
             }
             if (!kept) {
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) key[i] = ORD_NONE;
+                for (int i = 0; i < D; ++i) head[i] = ORD_EMPTY;
             }
         }
-        // ---- candidates
-        int best = ORD_NONE;
+        // ---- slots: lane j takes the j-th largest key and the lanes it was on (more than one: keys that agree but
+        // for what 64 bits will tell); lane k (k = 32: `next`) the one after the last slot
+        int mine = ORD_EMPTY, next = ORD_EMPTY;
+        unsigned from = 0;
+#pragma unroll 1
+        for (int j = 0; j <= p.k; ++j) {                      // past the last unmasked key: keys below ORD_LOWEST
+            const int hi = __reduce_max_sync(all, head[0]);
+            const bool taken = head[0] == hi;
+            const unsigned on = __ballot_sync(all, taken);
+            mine = lane == j ? hi : mine;
+            from = lane == j ? on : from;
+            if (j == MAX_TOPK) next = hi;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) best = max(best, key[i]);
-        int thr = ORD_NONE + 1;                               // any key that is not masked
-        if (m.sub >= 0) {
-            int blk = best;
-            for (int o = 1; o < (1 << m.sub); o <<= 1) blk = max(blk, __shfl_xor_sync(all, blk, o));
-            // lanes outside the groups that stay, or without experts, do not count
-            const bool counts = cnt > 0 && best != ORD_NONE;
-            const int lowest = __reduce_min_sync(all, counts ? blk : 0x7fffffff);
-            const int blocks = __popc(__ballot_sync(all, blk != ORD_NONE && (lane & ((1 << m.sub) - 1)) == 0));
-            if (blocks >= p.k) {
-                const float f = from_ordered(lowest);
-                thr = p.by_logit ? lowest : ordered(f - 2.0f * route_err_any(p.sigmoid, f, bmax) + 0.0f);
-                thr = max(thr, ORD_NONE + 1);
+            for (int i = 0; i + 1 < D; ++i) head[i] = taken ? head[i + 1] : head[i];
+            head[D - 1] = taken ? ORD_EMPTY : head[D - 1];
+            if (EPL > 4 && __any_sync(all, taken && head[0] == ORD_EMPTY && hi >= ORD_LOWEST)) {
+                if (taken) largest<EPL, D>(key, hi, head);
             }
         }
-        unsigned mask = 0;
-        uint32_t mask_hi = 0;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            if (i < 32) mask |= (unsigned)(key[i] >= thr) << (i & 31);
-            else mask_hi |= (uint32_t)(key[i] >= thr) << (i & 31);
-        }
-        const int mine = __popc(mask) + __popc(mask_hi);
-        int before = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(all, before, o);
-            if (lane >= o) before += v;
-        }
-        const int n = __shfl_sync(all, before, 31);
-        before -= mine;
-        int found;                                            // entries of o_*: min(k + 1, unmasked)
-        if (n <= ROUTE_CAND) {
-            int at = before;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                if (key[i] >= thr) {
-                    c_key[warp][at] = key[i];
-                    c_idx[warp][at] = e0 + i;
-                    c_l[warp][at] = l[i];
-                    ++at;
-                }
-            }
-            if (lane < 4) c_key[warp][n + lane] = ORD_NONE;   // whole vectors below
-            __syncwarp();
-            found = min(n, p.k + 1);
-            for (int a = lane; a < n; a += 32) {
-                const int ka = c_key[warp][a];
-                int rank = 0;
-                for (int j = 0; j < n; j += 4) {
-                    const int4 o = *reinterpret_cast<const int4*>(&c_key[warp][j]);
-                    rank += o.x > ka - (j < a);
-                    rank += o.y > ka - (j + 1 < a);
-                    rank += o.z > ka - (j + 2 < a);
-                    rank += o.w > ka - (j + 3 < a);
-                }
-                if (rank <= p.k) {
-                    o_key[warp][rank] = ka;
-                    o_idx[warp][rank] = c_idx[warp][a];
-                    o_l[warp][rank] = c_l[warp][a];
-                }
-            }
-        } else {
-            found = 0;
-            for (int j = 0; j <= p.k; ++j) {
-                const int hi = __reduce_max_sync(all, best);
-                if (hi == ORD_NONE) break;
-                const int owner = __ffs(__ballot_sync(all, best == hi)) - 1;
-                if (lane == owner) {
-                    bool taken = false;
-                    best = ORD_NONE;
-#pragma unroll
-                    for (int i = 0; i < EPL; ++i) {
-                        if (!taken && key[i] == hi) {
-                            taken = true;
-                            key[i] = ORD_NONE;
-                            o_key[warp][j] = hi;
-                            o_idx[warp][j] = e0 + i;
-                            o_l[warp][j] = l[i];
-                        }
-                        best = max(best, key[i]);
-                    }
-                }
-                found = j + 1;
-            }
-        }
-        __syncwarp();
-        // ---- slot j on lane j; the (k + 1)-th key is only compared with
+        sure = sure && (mine < ORD_LOWEST || (from & (from - 1)) == 0);
         int my_e = -1;
         float my_l = 0.0f;
-        if (lane < min(found, p.k)) {
-            my_e = o_idx[warp][lane];
-            my_l = o_l[warp][lane];
-            if (!p.by_logit && lane + 1 < found) {
-                const float ka = from_ordered(o_key[warp][lane]), kb = from_ordered(o_key[warp][lane + 1]);
-                const float lb = o_l[warp][lane + 1];
-                const float xa = p.sigmoid ? my_l : my_l - top, xb = p.sigmoid ? lb : lb - top;
-                const float sa = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-xa)) : __fdividef(__expf(xa), total);
-                const float sb = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-xb)) : __fdividef(__expf(xb), total);
-                sure = sure && ka - kb > route_err(p.sigmoid, sa, xa, ka) + route_err(p.sigmoid, sb, xb, kb);
-            }
+        if (mine >= ORD_LOWEST) {
+            const int q = __ffs(from) - 1;
+            my_e = (q >> m.lg) * m.each + (q & ((1 << m.lg) - 1)) * m.per + (POS - (mine & POS));
+            my_l = scored_logit(p, row, my_e);
         }
-        if (__all_sync(all, sure)) {
-            scored_weights(p, t, lane, my_e, my_l, top, total, m.kw);
+        // ---- is the order certain?
+        int after = __shfl_down_sync(all, mine, 1);
+        if (lane == 31) after = next;
+        const bool pair = lane < p.k && after >= ORD_LOWEST;
+        if (KIND == ROUTE_LOGIT) {
+            if (pair) sure = sure && (mine | POS) > (after | POS);
         } else {
-            route_token_f64(p, t, lane, route_keys + (size_t)warp * p.E);
+            const float ka = from_ordered(mine & ~POS), kb = from_ordered(after & ~POS);
+            constexpr bool SIG = KIND == ROUTE_SIGMOID;
+            const float x = SIG ? my_l : my_l - top;
+            const float s = SIG ? rcp_approx(1.0f + exp_approx(-x)) : exp_approx(x) * inv;
+            const float ea = route_err(SIG, s, x, ka);
+            float eb = __shfl_down_sync(all, ea, 1);
+            if (lane == 31) eb = route_err_any(SIG, kb, bmax);
+            if (pair) sure = sure && ka - kb > ea + eb + TRUNC * (fabsf(ka) + fabsf(kb));
         }
-        __syncwarp();                                         // o_*, c_* are free again
+        if (__all_sync(all, sure)) scored_weights(p, t, lane, my_e, my_l, top, total);
+        else route_token_f64(p, m, t, lane, route_keys + (size_t)warp * 32 * m.per);
     }
 }
 
