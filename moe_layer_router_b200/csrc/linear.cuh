@@ -266,7 +266,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int tile = blockIdx.x / p.split, slice = blockIdx.x - tile * p.split;   // K slice = cluster rank
     const int m_idx = tile % p.mt, n_idx = tile / p.mt;
     constexpr int FT = GATED ? 64 : 128;           // outputs per CTA
@@ -307,47 +307,47 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     grid_launch_next();
 
     if (warp == 0) {
-        if (lane == 0) {
-            const uint64_t pol_w = p.mt == 1 ? policy_evict_first() : policy_evict_normal();
-            const uint64_t pol_x = policy_evict_last();
-            const uint32_t bytes = LIN_A_BYTES + (uint32_t)x_bytes;
-            int issued = 0;
-            bool ok = true;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                const int s = issued % S;
-                if (!mbar_wait(empty_bar + s, ((issued / S) & 1) ^ 1u, abort_flag)) { ok = false; break; }
+        const uint64_t pol_w = p.mt == 1 ? policy_evict_first() : policy_evict_normal();
+        const uint64_t pol_x = policy_evict_last();
+        const uint32_t bytes = LIN_A_BYTES + (uint32_t)x_bytes;
+        int s = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait_warp(empty_bar + s, phase ^ 1u, abort_flag)) { ok = false; break; }
+            if (elect_one()) {
                 mbar_arrive_expect_tx(full_bar + s, bytes);
                 uint8_t* w_dst = sW + s * LIN_A_BYTES;
                 tma_load_2d(w_dst, &tmW, full_bar + s, kb * KB, n0, pol_w);
                 if (GATED) tma_load_2d(w_dst + 64 * 128, &tmWup, full_bar + s, kb * KB, n0, pol_w);
                 tma_load_2d(sX + s * x_bytes, &tmX, full_bar + s, kb * KB, t0, pol_x);
-                ++issued;
             }
-            if (!ok) {
-                const int n = issued < S ? issued : S;      // copies in flight land before exit
-                for (int i = 1; i <= n; ++i)
-                    mbar_wait(full_bar + ((issued - i) % S), (uint32_t)(((issued - i) / S) & 1), nullptr);
-            }
+            ++issued;
+            if (++s == S) { s = 0; phase ^= 1u; }
+        }
+        if (!ok) {
+            const int n = issued < S ? issued : S;          // copies in flight land before exit
+            for (int i = 1; i <= n; ++i)
+                mbar_wait(full_bar + ((issued - i) % S), (uint32_t)(((issued - i) / S) & 1), nullptr);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = F8 ? idesc_e4m3_f32(LIN_BM, p.bn) : idesc_bf16_f32(LIN_BM, p.bn);
-            for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
-                const int s = i % S;
-                if (!mbar_wait(full_bar + s, (i / S) & 1, abort_flag)) break;
-                tc_fence_after();
-                const uint64_t ad = smem_desc_k_sw128(sW + s * LIN_A_BYTES);
-                const uint64_t bd = smem_desc_k_sw128(sX + s * x_bytes);
+        const uint32_t idesc = F8 ? idesc_e4m3_f32(LIN_BM, p.bn) : idesc_bf16_f32(LIN_BM, p.bn);
+        const uint32_t a0 = smem_desc_lo(smem_u32(sW)), b0 = smem_desc_lo(smem_u32(sX));
+        int s = 0;
+        uint32_t phase = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait_warp(full_bar + s, phase, abort_flag)) break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t al = a0 + (uint32_t)s * (LIN_A_BYTES >> 4), bl = b0 + (uint32_t)s * (uint32_t)(x_bytes >> 4);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    if (F8) umma_e4m3(tmem_base, ad + 2ull * kk, bd + 2ull * kk, idesc, (i | kk) != 0);
-                    else umma_bf16(tmem_base, ad + 2ull * kk, bd + 2ull * kk, idesc, (i | kk) != 0);
-                }
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_lo<F8, false>(tmem_base, al + 2 * kk, bl + 2 * kk, idesc, kk > 0 || kb > kb0);
                 umma_commit(empty_bar + s);
             }
-            umma_commit(done_bar);       // all MMAs retired: the accumulator is final, the ring is idle
-            mbar_wait(done_bar, 0, nullptr);
+            if (++s == S) { s = 0; phase ^= 1u; }
         }
+        if (elect_one()) umma_commit(done_bar);      // all MMAs retired: the accumulator is final, the ring is idle
     } else if (warp < 4) {
         const int tid = threadIdx.x - 64;
         if (p.residual) {                                        // a row's segment is at most 3 lines of 128 bytes
@@ -782,7 +782,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
@@ -823,39 +823,40 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     grid_launch_next();
 
     if (warp == 0) {
-        if (lane == 0) {
-            const uint64_t pol_w = policy_evict_normal(), pol_x = policy_evict_last();
-            const uint32_t full_leader = map_to_cta(full_bar, 0);
-            const uint32_t bytes = 2u * (uint32_t)(LIN_A_BYTES + (p.bn / 2) * 128);
-            int stage = 0, issued = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int t = pair; t < total && ok; t += npairs) {
-                const LinearTile ti = linear_tile(p, t, nt);
-                const int n0 = (ti.n_idx * 2 + rank) * FT;
-                const int half = ((ti.ntok + 15) & ~15) >> 1;       // tokens per CTA of this tile
-                for (int kb = 0; kb < nk; ++kb) {
-                    if (!mbar_wait(empty_bar + stage, phase ^ 1u, abort_flag)) { ok = false; break; }
+        const uint64_t pol_w = policy_evict_normal(), pol_x = policy_evict_last();
+        const uint32_t full_leader = map_to_cta(full_bar, 0);
+        const uint32_t bytes = 2u * (uint32_t)(LIN_A_BYTES + (p.bn / 2) * 128);
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = pair; t < total && ok; t += npairs) {
+            const LinearTile ti = linear_tile(p, t, nt);
+            const int n0 = (ti.n_idx * 2 + rank) * FT;
+            const int x0 = ti.t0 + rank * (((ti.ntok + 15) & ~15) >> 1);       // this CTA's half of the tokens
+            for (int kb = 0; kb < nk; ++kb) {
+                if (!mbar_wait_warp(empty_bar + stage, phase ^ 1u, abort_flag)) { ok = false; break; }
+                if (elect_one()) {
                     const uint32_t fb = full_leader + (uint32_t)stage * 8u;
                     if (leader) mbar_arrive_expect_tx(full_bar + stage, bytes);
                     uint8_t* w_dst = sW + stage * LIN_A_BYTES;
                     tma_load_2d_pair(w_dst, &tmW, fb, kb * KB, n0, pol_w);
                     if (GATED) tma_load_2d_pair(w_dst + 64 * 128, &tmWup, fb, kb * KB, n0, pol_w);
-                    tma_load_2d_pair(sX + stage * 128 * 128, &tmX, fb, kb * KB, ti.t0 + rank * half, pol_x);
-                    ++issued;
-                    if (++stage == LINP_STAGES) { stage = 0; phase ^= 1u; }
+                    tma_load_2d_pair(sX + stage * 128 * 128, &tmX, fb, kb * KB, x0, pol_x);
                 }
+                ++issued;
+                if (++stage == LINP_STAGES) { stage = 0; phase ^= 1u; }
             }
-            if (!ok && leader) {
-                const int n = issued < LINP_STAGES ? issued : LINP_STAGES;
-                for (int i = 1; i <= n; ++i) {
-                    const int q = issued - i;
-                    mbar_wait(full_bar + (q % LINP_STAGES), (uint32_t)((q / LINP_STAGES) & 1), nullptr);
-                }
+        }
+        if (!ok && leader) {
+            const int n = issued < LINP_STAGES ? issued : LINP_STAGES;
+            for (int i = 1; i <= n; ++i) {
+                const int q = issued - i;
+                mbar_wait(full_bar + (q % LINP_STAGES), (uint32_t)((q / LINP_STAGES) & 1), nullptr);
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
+            const uint32_t a0 = smem_desc_lo(smem_u32(sW)), b0 = smem_desc_lo(smem_u32(sX));
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool any = false, ok = true;
@@ -863,30 +864,31 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 const LinearTile ti = linear_tile(p, t, nt);
                 const int n = (ti.ntok + 15) & ~15;
                 const uint32_t idesc = F8 ? idesc_e4m3_f32(256, n) : idesc_bf16_f32(256, n);
-                if (!mbar_wait(tempty_bar + acc, acc_phase ^ 1u, abort_flag)) break;
+                if (!mbar_wait_warp(tempty_bar + acc, acc_phase ^ 1u, abort_flag)) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)(acc * GEMM_ACC_COLS);
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (!mbar_wait(full_bar + stage, phase, abort_flag)) { ok = false; break; }
+                    if (!mbar_wait_warp(full_bar + stage, phase, abort_flag)) { ok = false; break; }
                     tc_fence_after();
-                    const uint64_t ad = smem_desc_k_sw128(sW + stage * LIN_A_BYTES);
-                    const uint64_t bd = smem_desc_k_sw128(sX + stage * 128 * 128);
+                    if (elect_one()) {
+                        const uint32_t al = a0 + (uint32_t)stage * (LIN_A_BYTES >> 4);
+                        const uint32_t bl = b0 + (uint32_t)stage * ((128 * 128) >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        if (F8) umma_e4m3_pair(d, ad + 2ull * kk, bd + 2ull * kk, idesc, (kb | kk) != 0);
-                        else umma_bf16_pair(d, ad + 2ull * kk, bd + 2ull * kk, idesc, (kb | kk) != 0);
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_lo<F8, true>(d, al + 2 * kk, bl + 2 * kk, idesc, kk > 0 || kb > 0);
+                        umma_commit_pair(empty_bar + stage, 0x3);
                     }
-                    umma_commit_pair(empty_bar + stage, 0x3);
                     any = true;
                     if (++stage == LINP_STAGES) { stage = 0; phase ^= 1u; }
                 }
                 if (!ok) break;
-                umma_commit_pair(tfull_bar + acc, 0x3);
+                if (elect_one()) umma_commit_pair(tfull_bar + acc, 0x3);
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1u;
             }
             if (any) {
-                umma_commit_pair(drain_bar, 0x1);
+                if (elect_one()) umma_commit_pair(drain_bar, 0x1);
+                __syncwarp();
                 mbar_wait(drain_bar, 0, nullptr);
             }
         }

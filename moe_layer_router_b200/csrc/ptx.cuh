@@ -346,6 +346,57 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t cta_mas
         : "memory");
 }
 
+// ---------------------------------------------------------------- issuing by a whole warp
+//
+// The tensor-core and TMA instructions take their operands from uniform registers.  In a loop that one lane runs
+// alone every operand is moved there first, and a k-block of four MMAs costs about 450 cycles of one thread's time;
+// in a loop that the warp runs together, with one elected lane issuing, the addresses stay uniform.
+
+// true for one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// The warp's index as a value the compiler knows to be the same in all lanes.
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+
+// mbar_wait by all lanes; the same answer in all of them.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+
+// smem_desc_k_sw128 in two words: the upper one is the same for every tile.
+constexpr uint32_t SMEM_DESC_K_SW128_HI = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t smem_addr) { return ((smem_addr >> 4) & 0x3FFFu) | (1u << 16); }
+
+// One tcgen05.mma with descriptors given by their lower words.
+template <bool F8, bool PAIR>
+__device__ __forceinline__ void umma_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                        uint32_t accumulate) {
+#define MOE_UMMA(GROUP, KIND)                                                                                 \
+    asm volatile(                                                                                             \
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"                                                          \
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"                                                    \
+        "setp.ne.b32 p, %4, 0;\n\t"                                                                           \
+        "tcgen05.mma." GROUP ".kind::" KIND " [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),                         \
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(SMEM_DESC_K_SW128_HI)                          \
+        : "memory")
+    if (PAIR) {
+        if (F8) MOE_UMMA("cta_group::2", "f8f6f4");
+        else MOE_UMMA("cta_group::2", "f16");
+    } else {
+        if (F8) MOE_UMMA("cta_group::1", "f8f6f4");
+        else MOE_UMMA("cta_group::1", "f16");
+    }
+#undef MOE_UMMA
+}
+
 // Shared-memory matrix descriptor for a K-major operand tile stored with the 128-byte
 // swizzle: rows of 64 bf16 (128 B), 8-row atoms of 1024 B stacked densely.
 //   bits  0-13 start address >> 4, 16-29 leading byte offset >> 4 (unused here, 1),
