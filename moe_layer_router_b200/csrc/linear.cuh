@@ -5,8 +5,8 @@
 // the fp32 accumulator multiplied by both.  Everything between the product and the one rounding to
 // bf16 is in fp32.
 //
-// Three kernels, chosen by run_linear_as():
-//   linear_rows_kernel   up to four tokens: a stream of weights through registers
+// Three kernels, chosen by run_linear_as() and plan_linear():
+//   linear_rows_kernel   one or two tokens: a stream of weights through registers
 //   linear_split_kernel  more tokens: 128 weight rows x up to 128 tokens per tile, K cut over a cluster
 //   linear_pair_kernel   many tokens: persistent CTA pairs, 256 weight rows x up to 256 tokens
 // In the last two the weights are the MMA's M side (D^T = W x^T), so few tokens cost no padded 128-row tile and
@@ -36,6 +36,7 @@ constexpr int LIN_BM = 128;                        // weight rows per tile
 constexpr int LIN_A_BYTES = LIN_BM * 128;          // one stage of weights: 128-byte rows
 constexpr int LIN_THREADS = 256;
 constexpr int LIN_MAX_SPLIT = 8;                   // portable cluster size
+constexpr int LIN_MAX_STAGES = 8;
 
 struct LinearParams {
     int M, N, K;
@@ -413,7 +414,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     else linear_join<F8, GATED, 8>(p, part, own, first, my_ntok, n0, nout, threadIdx.x);
 }
 
-// ---------------------------------------------------------------- up to four tokens: a warp per weight rows
+// ---------------------------------------------------------------- one or two tokens: a warp per weight rows
 //
 // A stream of weights with a few multiply-adds per element: four weight rows per warp (GATED: two of W and
 // the same two of W_up), each 16-byte piece of a row used for every token straight from registers, four warps
@@ -422,7 +423,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
 // linear_split_kernel, whose tile has to be set up, drained and joined around the loads, takes 11.4, 22.7 and
 // 10.6 us for these.
 constexpr int LINR_THREADS = 256;
-constexpr int LINR_MAX_TOKENS = 4;
+constexpr int LINR_MAX_TOKENS = 2;
 constexpr int LINR_WK = 4;                          // warps along K
 constexpr int LINR_GROUPS = LINR_THREADS / 32 / LINR_WK;   // and side by side along N
 
@@ -538,14 +539,19 @@ linear_rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ W, con
 // ---------------------------------------------------------------- many tokens: persistent CTA pairs
 //
 // Tiles of 256 weight rows x up to 256 tokens by CTA pairs (cta_group::2: each CTA holds 128 weight rows
-// and half of the tokens: 32 KB of operands per 64 K-elements for 256 x 128 outputs per SM), a 6-stage
-// ring and two accumulators, so that a tile's epilogue runs under the next tile's products.
+// and half of the tokens: 32 KB of operands per 64 K-elements for 256 x 128 outputs per SM), a ring of 6 to 10
+// stages and two accumulators, so that a tile's epilogue runs under the next tile's products.
 // The last token tile runs its MMAs with N = its tokens rounded up to 16.
-constexpr int LINP_STAGES = 6;
-constexpr int LINP_STAGE_BYTES = LIN_A_BYTES + 128 * 128;          // 128 weight rows + 128 tokens
+constexpr int LINP_MAX_STAGES = 10;
 constexpr int LINP_EPI_BYTES = 8 * 2 * 2048;                       // two 2 KB buffers per epilogue warp
 constexpr int LINP_THREADS = 320;                                  // TMA, MMA, 8 epilogue warps
-constexpr int LINP_SMEM_BYTES = LINP_STAGES * LINP_STAGE_BYTES + LINP_EPI_BYTES + 1024 + 256;
+constexpr int LINP_SMEM_BYTES = GEMM_SMEM_MAX;
+// 128 weight rows and half of the tile's tokens; 6 stages at 256 tokens, 10 at 32
+__host__ __device__ constexpr int linear_pair_stage_bytes(int bn) { return LIN_A_BYTES + bn / 2 * 128; }
+__host__ __device__ constexpr int linear_pair_stages(int bn) {
+    const int fit = (LINP_SMEM_BYTES - 1024 - 256 - LINP_EPI_BYTES) / linear_pair_stage_bytes(bn);
+    return fit < LINP_MAX_STAGES ? fit : LINP_MAX_STAGES;
+}
 // Token tiles walked together: the pairs' tiles of one moment are then about 8 x 9, near the fewest distinct
 // operand rows, and 8 tiles of 256 tokens stay in L2 while the weights pass by (all token tiles of M = 16384
 // would not).  4 to 16 measured alike.
@@ -772,11 +778,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                    const __grid_constant__ CUtensorMap tmX, const __grid_constant__ LinearParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int S = p.stages, x_bytes = p.bn / 2 * 128;
     uint8_t* sW = smem;
-    uint8_t* sX = smem + LINP_STAGES * LIN_A_BYTES;
-    uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + LINP_STAGES * LINP_STAGE_BYTES + LINP_EPI_BYTES);
-    uint64_t* empty_bar = full_bar + LINP_STAGES;
-    uint64_t* tfull_bar = empty_bar + LINP_STAGES;
+    uint8_t* sX = smem + S * LIN_A_BYTES;
+    uint8_t* rows = sX + S * x_bytes;                               // the epilogue's, see LinearWarp
+    uint64_t* full_bar = reinterpret_cast<uint64_t*>(rows + LINP_EPI_BYTES);
+    uint64_t* empty_bar = full_bar + S;
+    uint64_t* tfull_bar = empty_bar + S;
     uint64_t* tempty_bar = tfull_bar + 2;
     uint64_t* drain_bar = tempty_bar + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
@@ -793,7 +801,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     const int total = nt * p.mt;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < LINP_STAGES; ++s) {
+        for (int s = 0; s < S; ++s) {
             mbar_init(full_bar + s, 1);
             mbar_init(empty_bar + s, 1);
         }
@@ -825,7 +833,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     if (warp == 0) {
         const uint64_t pol_w = policy_evict_normal(), pol_x = policy_evict_last();
         const uint32_t full_leader = map_to_cta(full_bar, 0);
-        const uint32_t bytes = 2u * (uint32_t)(LIN_A_BYTES + (p.bn / 2) * 128);
+        const uint32_t bytes = 2u * (uint32_t)(LIN_A_BYTES + x_bytes);
         int stage = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -841,17 +849,17 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                     uint8_t* w_dst = sW + stage * LIN_A_BYTES;
                     tma_load_2d_pair(w_dst, &tmW, fb, kb * KB, n0, pol_w);
                     if (GATED) tma_load_2d_pair(w_dst + 64 * 128, &tmWup, fb, kb * KB, n0, pol_w);
-                    tma_load_2d_pair(sX + stage * 128 * 128, &tmX, fb, kb * KB, x0, pol_x);
+                    tma_load_2d_pair(sX + stage * x_bytes, &tmX, fb, kb * KB, x0, pol_x);
                 }
                 ++issued;
-                if (++stage == LINP_STAGES) { stage = 0; phase ^= 1u; }
+                if (++stage == S) { stage = 0; phase ^= 1u; }
             }
         }
         if (!ok && leader) {
-            const int n = issued < LINP_STAGES ? issued : LINP_STAGES;
+            const int n = issued < S ? issued : S;
             for (int i = 1; i <= n; ++i) {
                 const int q = issued - i;
-                mbar_wait(full_bar + (q % LINP_STAGES), (uint32_t)((q / LINP_STAGES) & 1), nullptr);
+                mbar_wait(full_bar + (q % S), (uint32_t)((q / S) & 1), nullptr);
             }
         }
     } else if (warp == 1) {
@@ -872,14 +880,14 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                     tc_fence_after();
                     if (elect_one()) {
                         const uint32_t al = a0 + (uint32_t)stage * (LIN_A_BYTES >> 4);
-                        const uint32_t bl = b0 + (uint32_t)stage * ((128 * 128) >> 4);
+                        const uint32_t bl = b0 + (uint32_t)stage * (uint32_t)(x_bytes >> 4);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             umma_lo<F8, true>(d, al + 2 * kk, bl + 2 * kk, idesc, kk > 0 || kb > 0);
                         umma_commit_pair(empty_bar + stage, 0x3);
                     }
                     any = true;
-                    if (++stage == LINP_STAGES) { stage = 0; phase ^= 1u; }
+                    if (++stage == S) { stage = 0; phase ^= 1u; }
                 }
                 if (!ok) break;
                 if (elect_one()) umma_commit_pair(tfull_bar + acc, 0x3);
@@ -899,7 +907,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         const bool up = GATED && sub >= 2;
         const int bar = 1 + part + 2 * half;                        // GATED: the pair's barrier
         const int tid = threadIdx.x - 64;
-        uint8_t* rows = reinterpret_cast<uint8_t*>(smem + LINP_STAGES * LINP_STAGE_BYTES);
         uint8_t* mine = rows + (sub + 4 * half) * 2048;             // 2 KB; the second set 16 KB further on
         uint8_t* other = rows + ((sub ^ 2) + 4 * half) * 2048;
         const uint32_t tempty_leader = map_to_cta(tempty_bar, 0);
@@ -908,7 +915,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         for (int t = pair; t < total; t += npairs) {
             const LinearTile ti = linear_tile(p, t, nt);
             const int n0 = (ti.n_idx * 2 + rank) * FT, nout = min(FT, p.N - n0);
-            const int c0 = half * 128, c1 = min(c0 + 128, ti.ntok);
+            const int share = (p.bn / 2 + 31) & ~31;                  // tokens of the first half
+            const int c0 = half * share, c1 = min(half ? p.bn : share, ti.ntok);
             LinearWarp<F8, GATED> e;
             e.begin(p, n0 + part * 32, up, lane);
             if (p.residual && e.vec && c0 < c1) e.load_residual(p, ti.t0 + c0, c1 - c0, lane);

@@ -1354,29 +1354,80 @@ int linear_maps(const LinearArgs& a, int x_rows, CUtensorMap* mW, CUtensorMap* m
     return mk(mX, a.x, a.M, x_rows);
 }
 
-// Tiles of linear_split_kernel.  Token tiles: one up to 128 tokens, then tiles of about 128; short K (up to
-// 24 k-blocks) prefers tiles of 64, whose sums are joined sooner (512 x 512, 512 tokens: 5.6 us against 6.8).
-// K slices: doubled while the tiles do not fill two CTAs per SM and each slice keeps 2 k-blocks, beyond 128 CTAs
-// only while it keeps 14 (32 tiles at K = 4096, 16 tokens: 4 slices 11.0 us, 8 11.4; at K = 14336: 26.4,
-// 23.9).  Over 290 combinations of sizes and types this rule is 3 % off the best of all tiles and slices.
+// How a dense layer runs: linear_pair_kernel (pair) or linear_split_kernel, with `bn` tokens per tile, `split` K
+// slices and `stages` ring slots, as the one whose estimated time is least.  The estimate, in us:
+//   3.9 for the launch, the set-up and the first and last bytes, and the larger of
+//     all bytes at 6.4 TB/s, and
+//     the operands that pass into the busiest SM at 90 GB/s, 47 bytes per cycle (a tile's products, 2 bn cycles per
+//     k-block, take less);
+//   0.2 per wave of pair tiles; for `split` K slices 0.5 + 0.1 split + 0.026 bn, their hand-over and joining.
+// Measured, in us, bf16 with residual: 512 x 4096 x 4096 pair, bn 128: 18.6, split, bn 128: 23.5; 256 x 7168 x 2048 pair,
+// bn 128: 12.6, split, bn 128, 2 slices: 17.4; 256 x 2048 x 7168 pair, bn 64: 24.0, split, bn 128, 4 slices: 15.1; 24 x 512
+// x 512 pair: 4.6, split, 8 slices: 4.0.  Over 238 combinations of sizes and types the choice is 2.5 % off the
+// best of all tiles and slices (geometric mean).
+struct LinearPlan {
+    bool pair;
+    int bn, split, stages;
+    float us;
+};
+
+int linear_split_stages(int bn, int split, bool own_part, int ctas_per_sm) {
+    const int part = linear_part_bytes(bn, split), stage = LIN_A_BYTES + bn * 128;
+    const int room = GEMM_SMEM_MAX / ctas_per_sm - (ctas_per_sm > 1 ? 1024 : 0) - 1024 - 256 - (own_part ? part : 0);
+    int stages = std::min(LIN_MAX_STAGES, room / stage);
+    if (!own_part)      // the ring holds the partial sums
+        while (stages * stage < part) ++stages;
+    return stages;
+}
+
+LinearPlan plan_linear(int sms, long long M, long long N, long long K, bool f8, bool gated, bool residual) {
+    const float kStart = 3.9f, kIn = 90e3f;       // us, bytes per us
+    const int nk = (int)((K + (f8 ? 127 : 63)) / (f8 ? 128 : 64));
+    const float dram = ((gated ? 2 : 1) * (float)N * K * (f8 ? 1 : 2) + (float)M * K * (f8 ? 1 : 2) +
+                        (float)M * N * (residual ? 4 : 2)) / 6.4e6f;
+    LinearPlan best = {false, 0, 1, 0, 3e38f};
+    // pairs: 256 weight rows, bn tokens; tiles in waves of sms / 2
+    const long long pairs = sms / 2, nt2 = (N + (gated ? 127 : 255)) / (gated ? 128 : 256);
+    for (int bn = 256; bn >= 32; bn -= bn > 128 ? 16 : 32) {
+        if (bn - (bn > 128 ? 16 : 32) >= M) continue;                 // a smaller tile holds all tokens
+        const long long tiles = nt2 * ((M + bn - 1) / bn), waves = (tiles + pairs - 1) / pairs;
+        const float kb = linear_pair_stage_bytes(bn) / kIn;
+        const float us = kStart + std::max((float)waves * nk * kb, dram) + 0.2f * waves;
+        if (us < best.us) best = {true, bn, 1, linear_pair_stages(bn), us};
+    }
+    // K slices over a cluster: 128 weight rows, bn tokens
+    const long long nt1 = (N + (gated ? 63 : 127)) / (gated ? 64 : 128);
+    for (int want = 128; want >= 64; want /= 2) {
+        const long long mt = (M + want - 1) / want;
+        const int bn = (int)(((M + mt - 1) / mt + 15) / 16 * 16);
+        const long long tiles = nt1 * ((M + bn - 1) / bn);
+        for (int split = 1; split <= LIN_MAX_SPLIT && split <= nk; split *= 2) {
+            const long long ctas = tiles * split, per_sm = (ctas + sms - 1) / sms;
+            if (split > 1 && per_sm > 2) break;
+            const bool own_part = split > 1 && bn <= 32;
+            // clusters of eight one CTA per SM do not all find room at once (32 x 2048 x 7168: 16.0 us against 9.8)
+            const int together = per_sm > 1 || split == 8 ? 2 : 1;
+            const int stages = linear_split_stages(bn, split, own_part, together);
+            const float kb = (LIN_A_BYTES + 128 * bn) / kIn;
+            const int slice = (nk + split - 1) / split;
+            const float us = kStart + std::max((float)per_sm * slice * kb, dram) + (split > 1 ? 0.5f + 0.1f * split + 0.026f * bn : 0.0f);
+            if (us < best.us) best = {false, bn, split, stages, us};
+        }
+    }
+    return best;
+}
+
 template <bool F8, bool GATED>
-int launch_linear_split(const LinearArgs& a, cudaStream_t s) {
+int launch_linear_split(const LinearArgs& a, const LinearPlan& plan, cudaStream_t s) {
     LinearParams p = linear_params(a);
     const int nt = (a.N + (GATED ? 63 : 127)) / (GATED ? 64 : 128);
-    const int nk = (a.K + (F8 ? 127 : 63)) / (F8 ? 128 : 64);
-    const int mt0 = a.M <= 64 ? 1 : nk <= 24 && a.M <= 1024 ? (a.M + 63) / 64 : (a.M + 127) / 128;
-    p.bn = ((a.M + mt0 - 1) / mt0 + 15) / 16 * 16;
+    p.bn = plan.bn;
+    p.split = plan.split;
+    p.stages = plan.stages;
     p.mt = (a.M + p.bn - 1) / p.bn;
     p.tmem_cols = p.bn <= 32 ? 32 : p.bn <= 64 ? 64 : 128;
-    const long long tiles = (long long)nt * p.mt;
-    p.split = 1;
-    while (p.split < LIN_MAX_SPLIT && tiles * p.split * 2 <= 256 && nk / (p.split * 2) >= 2 &&
-           (tiles * p.split < 128 || nk / (p.split * 2) >= 14))
-        p.split *= 2;
     p.own_part = p.split > 1 && p.bn <= 32;
-    // a ring that leaves room for two CTAs per SM, and holds the partial sums
-    p.stages = 4 * (LIN_A_BYTES + p.bn * 128) <= 112000 ? 4 : 3;
-    while (!p.own_part && p.stages * (LIN_A_BYTES + p.bn * 128) < linear_part_bytes(p.bn, p.split)) ++p.stages;
+    const long long tiles = (long long)nt * p.mt;
     if (tiles * p.split >= (1ll << 31)) return MOE_ERR_SHAPE;
     CUtensorMap mW, mWup, mX;
     int rc = linear_maps<F8, GATED>(a, p.bn, &mW, &mWup, &mX);
@@ -1394,23 +1445,13 @@ int launch_linear_split(const LinearArgs& a, cudaStream_t s) {
 }
 
 template <bool F8, bool GATED>
-int launch_linear_pair(DeviceInfo* di, const LinearArgs& a, cudaStream_t s) {
+int launch_linear_pair(DeviceInfo* di, const LinearArgs& a, const LinearPlan& plan, cudaStream_t s) {
     LinearParams p = linear_params(a);
     const int nt = (a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
-    // tokens per tile: the fewest cycles over whole waves of pairs, a k-block taking 2 bn cycles of products or
-    // 16 KB of weights and 64 bn bytes of tokens at about 70 B per clock (2048 x 4096 x 4096 is two waves either
-    // way: 54.8 us at 256, 51.3 at 240)
     const long long pairs = di->sms / 2;
-    long long best = -1;
-    for (int bn = 256; bn >= 128; bn -= 16) {
-        const long long t = (long long)nt * ((a.M + bn - 1) / bn), waves = (t + pairs - 1) / pairs;
-        const long long cost = waves * (std::max(2 * bn, (16384 + 64 * bn) / 70) + 64);
-        if (best < 0 || cost < best) {
-            best = cost;
-            p.bn = bn;
-        }
-    }
+    p.bn = plan.bn;
     p.mt = (a.M + p.bn - 1) / p.bn;
+    p.stages = plan.stages;
     const long long tiles = (long long)nt * p.mt;
     if (tiles >= (1ll << 30)) return MOE_ERR_SHAPE;
     CUtensorMap mW, mWup, mX;
@@ -1436,8 +1477,7 @@ int launch_linear_rows(const LinearArgs& a, cudaStream_t s) {
     const uint4 *x = static_cast<const uint4*>(a.x), *W = static_cast<const uint4*>(a.W),
                 *U = static_cast<const uint4*>(a.W_up);
     const cudaError_t e = a.M == 1   ? cudaLaunchKernelEx(&cfg, linear_rows_kernel<1, GATED>, x, W, U, p)
-                          : a.M == 2 ? cudaLaunchKernelEx(&cfg, linear_rows_kernel<2, GATED>, x, W, U, p)
-                                     : cudaLaunchKernelEx(&cfg, linear_rows_kernel<4, GATED>, x, W, U, p);
+                                        : cudaLaunchKernelEx(&cfg, linear_rows_kernel<2, GATED>, x, W, U, p);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
@@ -1445,21 +1485,14 @@ int launch_linear_rows(const LinearArgs& a, cudaStream_t s) {
     return MOE_OK;
 }
 
-// Which kernel.  Rows: one or two tokens always, three and four while the weights are few (4096 x 4096: 10.1 us
-// against 11.4; 14336 x 4096: 30.2 against 22.6, its multiply-adds then take longer than the loads).  Pairs: once
-// their tiles fill most of the GPU's 74 pairs, or for short K from 1024 tokens on (768 x 4096 x 4096: 30 us
-// against 38; 512: 27.2 against 25.0; 1536 x 1000 x 1384: 15.7 against 18.5).
+// One or two bf16 tokens: a warp per weight rows (see linear_rows_kernel); otherwise by plan_linear().
 template <bool F8, bool GATED>
 int run_linear_as(DeviceInfo* di, const LinearArgs& a, cudaStream_t s) {
-    const long long elems = (long long)a.N * a.K * (GATED ? 2 : 1);
     if constexpr (!F8) {
-        if (a.M <= 2 || (a.M <= LINR_MAX_TOKENS && elems <= (1ll << 24))) return launch_linear_rows<GATED>(a, s);
+        if (a.M <= LINR_MAX_TOKENS) return launch_linear_rows<GATED>(a, s);
     }
-    const long long tiles = (long long)((a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256)) * ((a.M + 255) / 256);
-    const int nk = (a.K + (F8 ? 127 : 63)) / (F8 ? 128 : 64);
-    if (a.M > 128 && (tiles >= 40 || (tiles >= 16 && nk <= 24 && a.M >= 1024)))
-        return launch_linear_pair<F8, GATED>(di, a, s);
-    return launch_linear_split<F8, GATED>(a, s);
+    const LinearPlan plan = plan_linear(di->sms, a.M, a.N, a.K, F8, GATED, a.residual != nullptr);
+    return plan.pair ? launch_linear_pair<F8, GATED>(di, a, plan, s) : launch_linear_split<F8, GATED>(a, plan, s);
 }
 
 template <bool F8>
