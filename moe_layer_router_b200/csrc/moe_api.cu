@@ -444,36 +444,61 @@ int run_route_scored(DeviceInfo* di, const float* logits, int nsplit, float* log
     p.idx = idx;
     p.w = w;
     // lanes: the largest power of two per group, its experts spread evenly over them
-    RouteLanes m;
-    m.lg = 0;
-    while ((2 << m.lg) * r.n_group <= 32) ++m.lg;
     const int each = E / r.n_group;
-    m.per = (each + (1 << m.lg) - 1) >> m.lg;
-    m.each = each;
+    auto lanes = [&](int of) {
+        RouteLanes m;
+        m.lg = 0;
+        while ((2 << m.lg) * r.n_group <= of) ++m.lg;
+        m.per = (each + (1 << m.lg) - 1) >> m.lg;
+        m.each = each;
+        return m;
+    };
+    const RouteLanes warp = lanes(32);
+    // two tokens per warp once there are more of them than warps on the GPU at a time (measured: 32768 x 256, 8
+    // groups, 44 us with one, below with two)
+    const bool two = k < 16 && r.n_group <= 16 && lanes(16).per <= 16 && T > 32ll * di->sms;
+    const RouteLanes m = two ? lanes(16) : warp;
     const bool vec = nsplit == 1 && m.per % 4 == 0 && each % 4 == 0;
-    const size_t smem = (size_t)ROUTE_WARPS * 32 * m.per * sizeof(double);
-    const unsigned grid = (unsigned)std::min<long long>(((long long)T + ROUTE_WARPS - 1) / ROUTE_WARPS, 4ll * di->sms);
+    const size_t smem = (size_t)ROUTE_WARPS * 32 * warp.per * sizeof(double);
+    const int per_block = ROUTE_WARPS * (two ? 2 : 1);
+    const long long blocks = ((long long)T + per_block - 1) / per_block;
     const int kind = p.by_logit ? ROUTE_LOGIT : p.sigmoid ? ROUTE_SIGMOID : ROUTE_SOFTMAX;
     cudaLaunchConfig_t cfg;
-    const LaunchAttrs attrs(&cfg, grid, ROUTE_WARPS * 32, smem, s, 1);
+    const LaunchAttrs attrs(&cfg, 1, ROUTE_WARPS * 32, smem, s, 1);
     int rc = MOE_OK;
     cudaError_t e = cudaSuccess;
-#define MOE_ROUTE_KIND(EPL, VEC, KIND)                                                                            \
-    if ((rc = opt_in_smem<route_scored_kernel<EPL, VEC, KIND>, ROUTE_WARPS * 32 * EPL * 8>()) == MOE_OK)          \
-        e = cudaLaunchKernelEx(&cfg, route_scored_kernel<EPL, VEC, KIND>, p, m);
-#define MOE_ROUTE(EPL, VEC)                                                                                       \
+    // one wave of blocks, each warp taking token after token
+#define MOE_ROUTE_KIND(LPT, EPL, VEC, KIND)                                                                       \
+    {                                                                                                             \
+        constexpr auto kernel = route_scored_kernel<LPT, EPL, VEC, KIND>;                                         \
+        if ((rc = opt_in_smem<kernel, ROUTE_WARPS * 32 * EPL * 8>()) == MOE_OK) {                                 \
+            int per_sm = 1;                                                                                       \
+            if (blocks > di->sms &&                                                                               \
+                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, ROUTE_WARPS * 32, smem) != cudaSuccess) \
+                return MOE_ERR_CUDA;                                                                              \
+            cfg.gridDim.x = (unsigned)std::min<long long>(blocks, (long long)std::max(per_sm, 1) * di->sms);      \
+            e = cudaLaunchKernelEx(&cfg, kernel, p, m, warp);                                                     \
+        }                                                                                                         \
+    }
+#define MOE_ROUTE(LPT, EPL, VEC)                                                                                  \
     do {                                                                                                          \
-        if (kind == ROUTE_LOGIT) { MOE_ROUTE_KIND(EPL, VEC, ROUTE_LOGIT) }                                        \
-        else if (kind == ROUTE_SIGMOID) { MOE_ROUTE_KIND(EPL, VEC, ROUTE_SIGMOID) }                               \
-        else { MOE_ROUTE_KIND(EPL, VEC, ROUTE_SOFTMAX) }                                                          \
+        if (kind == ROUTE_LOGIT) { MOE_ROUTE_KIND(LPT, EPL, VEC, ROUTE_LOGIT) }                                   \
+        else if (kind == ROUTE_SIGMOID) { MOE_ROUTE_KIND(LPT, EPL, VEC, ROUTE_SIGMOID) }                          \
+        else { MOE_ROUTE_KIND(LPT, EPL, VEC, ROUTE_SOFTMAX) }                                                     \
     } while (0)
-    if (m.per <= 1) MOE_ROUTE(1, false);
-    else if (m.per <= 2) MOE_ROUTE(2, false);
-    else if (m.per <= 4) { if (vec) MOE_ROUTE(4, true); else MOE_ROUTE(4, false); }
-    else if (m.per <= 8) { if (vec) MOE_ROUTE(8, true); else MOE_ROUTE(8, false); }
-    else if (m.per <= 16) MOE_ROUTE(16, false);
-    else if (m.per <= 32) MOE_ROUTE(32, false);
-    else MOE_ROUTE(64, false);
+    if (two) {
+        if (m.per <= 1) MOE_ROUTE(16, 1, false);
+        else if (m.per <= 4) { if (vec) MOE_ROUTE(16, 4, true); else MOE_ROUTE(16, 4, false); }
+        else if (m.per <= 8) { if (vec) MOE_ROUTE(16, 8, true); else MOE_ROUTE(16, 8, false); }
+        else { if (vec) MOE_ROUTE(16, 16, true); else MOE_ROUTE(16, 16, false); }
+    }
+    else if (m.per <= 1) MOE_ROUTE(32, 1, false);
+    else if (m.per <= 2) MOE_ROUTE(32, 2, false);
+    else if (m.per <= 4) { if (vec) MOE_ROUTE(32, 4, true); else MOE_ROUTE(32, 4, false); }
+    else if (m.per <= 8) { if (vec) MOE_ROUTE(32, 8, true); else MOE_ROUTE(32, 8, false); }
+    else if (m.per <= 16) MOE_ROUTE(32, 16, false);
+    else if (m.per <= 32) MOE_ROUTE(32, 32, false);
+    else MOE_ROUTE(32, 64, false);
 #undef MOE_ROUTE_KIND
 #undef MOE_ROUTE
     if (rc != MOE_OK) return rc;

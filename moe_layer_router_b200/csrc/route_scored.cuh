@@ -65,41 +65,63 @@ __device__ __forceinline__ float exp_approx(float x) {
     return r;
 }
 
+// Over the LPT lanes of a token (32: the warp; 16: each half of it for itself): the largest, the sum, a ballot.
+template <int LPT>
+__device__ __forceinline__ int lanes_max(int v) {
+    if constexpr (LPT == 32) {
+        return __reduce_max_sync(0xffffffffu, v);
+    } else {
+#pragma unroll
+        for (int o = LPT / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+        return v;
+    }
+}
+template <int LPT>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <int LPT>
+__device__ __forceinline__ unsigned lanes_ballot(bool v) {
+    const unsigned b = __ballot_sync(0xffffffffu, v);
+    return LPT == 32 ? b : (threadIdx.x & 16 ? b >> 16 : b & 0xffffu);
+}
+
 // The weights of the selected experts: lane j < k holds slot j's expert (-1: none) and logit.
 // top / total: the row's largest logit and sum of e^(l - top) over its unmasked experts (softmax
 // without renormalisation).  Renormalised weights are ratios of scores, taken relative to the largest
 // selected one where they would underflow: s_j ~ e^(l_j - m) in softmax, and in sigmoid once all selected
-// logits are below -60.  Warp-collective.
-__device__ __forceinline__ void scored_weights(const RouteScored& p, long long t, int lane, int my_e, float my_l,
-                                               float top, float total) {
+// logits are below -60.  LPT lanes per token, `lane` among them; warp-collective, writing where `live`.
+template <int LPT>
+__device__ __forceinline__ void scored_weights(const RouteScored& p, long long t, bool live, int lane, int my_e,
+                                               float my_l, float top, float total) {
     const bool have = lane < p.k && my_e >= 0;
     float s = 0.0f;
     if (!p.sigmoid) {
         if (p.renorm) {      // as moe_route computes them: the same weights, bit for bit
-            const float m = from_ordered(__reduce_max_sync(0xffffffffu, ordered((have ? my_l : -INFINITY) + 0.0f)));
+            const float m = from_ordered(lanes_max<LPT>(ordered((have ? my_l : -INFINITY) + 0.0f)));
             if (have) s = expf(my_l - m);
-            s /= warp_sum(s);
+            s /= lanes_sum<LPT>(s);
         } else if (have) {
             s = expf(my_l - top) / total;
         }
     } else {
         if (have) s = rcp_approx(1.0f + exp_approx(-my_l));   // a few ulp
         if (p.renorm) {
-            if (!__any_sync(0xffffffffu, have && my_l > -60.0f)) {
-                const float m = from_ordered(__reduce_max_sync(0xffffffffu, ordered(have ? my_l : -INFINITY)));
-                if (have) s = expf(my_l - m);                 // 1 + e^l is 1
-            }
-            s *= rcp_approx(warp_sum(s));
+            const float m = from_ordered(lanes_max<LPT>(ordered(have ? my_l : -INFINITY)));
+            if (have && m < -60.0f) s = expf(my_l - m);       // 1 + e^l is 1
+            s *= rcp_approx(lanes_sum<LPT>(s));
         }
     }
-    if (lane < p.k) {
+    if (live && lane < p.k) {
         p.idx[t * p.k + lane] = have ? my_e : -1;
         p.w[t * p.k + lane] = have ? s * p.scale : 0.0f;
     }
 }
 
-// Experts of a warp's lanes: group g on 2^lg lanes, each holding up to `per` consecutive experts (the last lanes of
-// a group fewer), so that (lane, position) is the order of the experts.
+// Experts of a token's lanes (a warp, or half of one): group g on 2^lg lanes, each holding up to `per` consecutive
+// experts (the last lanes of a group fewer), so that (lane, position) is the order of the experts.
 struct RouteLanes {
     int lg, per;
     int each;     // E / n_group
@@ -202,36 +224,41 @@ __device__ __noinline__ void route_token_f64(const RouteScored& p, const RouteLa
         }
     }
     const float my_l = my_e >= 0 ? scored_logit(p, row, my_e) : 0.0f;
-    scored_weights(p, t, lane, my_e, my_l, top, (float)total);
+    scored_weights<32>(p, t, true, lane, my_e, my_l, top, (float)total);
 }
 
 // ---------------------------------------------------------------- the kernel: keys in 32 bits
 //
-// One warp per token, its experts on the lanes as RouteLanes has them, EPL >= per.  Keys are integers of the floats' order whose
+// One warp per token, or two tokens per warp, the experts on the lanes as RouteLanes has them, EPL >= per.  Keys are integers of the floats' order whose
 // last BITS bits hold the position in the lane: a comparison carries the expert along and a lane's keys are distinct.
 //   lanes       sort their four largest keys (8 experts: 32 minima and maxima)
 //   groups      the two largest keys merged over the group's lanes; rank by n_group shuffles
-//   slots       k + 1 times: the warp's largest list head (one redux), taken off its lane's list; a lane whose four
-//               are used up sorts its next four
-//   certainty   keys are off by at most route_err and 2^BITS steps.  Where two neighbours in the order, or the last
-//               group that stays and the first that does not, are closer than that, the token is done again
-//               in 64 bits (route_token_f64): about one token in 500 for scores of unit variance, 256 experts
+//   slots       k + 1 times: the largest list head, taken off its lane's list; a lane whose four are used up sorts its
+//               next four
+//   certainty   keys are off by at most route_err and 2^BITS steps.  Neighbours in the order that are closer than that
+//               are put in order by 64-bit keys of the slots alone (one token in 400 for scores of unit variance, 256
+//               experts); where it is the last slot and the key after it, or the last group that stays and the first
+//               that does not, the token is done again in 64 bits (route_token_f64: one in some thousands)
 // Bound by the instructions, not by the 33.5 MB of logits that 32768 x 256 has (5.2 us at the measured copy rate).
 constexpr int ROUTE_WARPS = 8;
 
 // Errors in units of 2^-23.  The fast exponential of x is off by at most 2 + 1.16 |x| of its value (x = -l, or
-// l - top in softmax, whose rounding adds |x| / 2), the divide by 2.
-//   sigmoid  the exponential's part reaches s by the factor 1 - s: s (5 + 1.25 |x|)
+// l - top in softmax, whose rounding adds |x| / 2), the fast reciprocal by 1, a rounding by 1/2.
+//   sigmoid  the exponential's part reaches s by the factor 1 - s: s (2 + (1 - s) (2 + 1.25 |x|))
 //   softmax  the sum adds its terms' mean error, at most 2 + 1.7 ln E, and its roundings, at most (E / 32 + 5) / 2:
 //            s (40 + 2.5 |x|) for E <= 1024
 // and the key's rounding half of |key|.  route_err: of a key whose score and x are known.  route_err_any: of any
-// key with that value; sigmoid: s (1 - s) |x| < 0.23; softmax: s <= |key| + bmax, and |x| <= 40 or s < 1e-17.
+// key with that value: sigmoid, s <= min(1, S) with S = |key| + bmax, and s (1 - s) (2 + 1.25 |x|) < 0.8; softmax,
+// s <= S and s |x| <= s ln(1 / s), which grows with s up to 1 / e.
 __device__ __forceinline__ float route_err(bool sigmoid, float s, float x, float key) {
-    const float rel = sigmoid ? fmaf(1.25f, fabsf(x), 5.0f) : fmaf(2.5f, fabsf(x), 40.0f);
+    const float rel = sigmoid ? fmaf(1.0f - s, fmaf(1.25f, fabsf(x), 2.0f), 2.0f) : fmaf(2.5f, fabsf(x), 40.0f);
     return 1.1920929e-7f * fmaf(s, rel, fabsf(key)) + 1e-36f;
 }
 __device__ __forceinline__ float route_err_any(bool sigmoid, float key, float bmax) {
-    return sigmoid ? 4.8e-7f * (1.0f + fabsf(key) + bmax) : 1.7e-5f * (fabsf(key) + 2.0f * bmax) + 1e-17f;
+    const float S = fabsf(key) + bmax;
+    if (sigmoid) return 1.1920929e-7f * (2.0f * fminf(S, 1.0f) + 0.8f + fabsf(key));
+    const float sx = S < 0.36f ? -S * __logf(S + 1e-30f) : 0.37f;
+    return 1.1920929e-7f * (41.0f * S + 2.5f * sx) + 1e-36f;
 }
 
 __device__ __forceinline__ void order2(int& a, int& b) {      // a >= b
@@ -269,43 +296,50 @@ __device__ __forceinline__ void largest(const int (&key)[EPL], int bound, int (&
 
 enum { ROUTE_LOGIT = 0, ROUTE_SIGMOID = 1, ROUTE_SOFTMAX = 2 };   // what a key is
 
-template <int EPL, bool VEC, int KIND>
-__global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 4 : 1) route_scored_kernel(const __grid_constant__ RouteScored p,
-                                                                        const __grid_constant__ RouteLanes m) {
-    extern __shared__ double route_keys[];      // route_token_f64: 32 `per` doubles per warp
+// LPT lanes per token: 32, or 16 with a token on each half of the warp, which shares all that goes over the lanes
+// (k < 16, at most 16 experts per lane).
+template <int LPT, int EPL, bool VEC, int KIND>
+__global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 4 : EPL <= 16 && LPT == 16 ? 3 : 1)
+route_scored_kernel(const __grid_constant__ RouteScored p, const __grid_constant__ RouteLanes m,
+                    const __grid_constant__ RouteLanes m64) {
+    extern __shared__ double route_keys[];      // route_token_f64: 32 m64.per doubles per warp
+    constexpr int TOKENS = 32 / LPT;            // of a warp
     constexpr int BITS = EPL <= 1 ? 0 : EPL <= 2 ? 1 : EPL <= 4 ? 2 : EPL <= 8 ? 3 : EPL <= 16 ? 4 : EPL <= 32 ? 5 : 6;
     constexpr int POS = (1 << BITS) - 1;
     constexpr int D = EPL < 4 ? EPL : 4;
     constexpr float TRUNC = 1.1920929e-7f * (1 << BITS);       // relative, of the position's bits
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & (LPT - 1), warp = threadIdx.x >> 5, half = (threadIdx.x & 31) / LPT;
     const unsigned all = 0xffffffffu;
     const RouteLane at(p, m, lane);
     const int g = at.group, e0 = at.e0, cnt = at.cnt;
+    // the bias, NaN and +inf as -inf (reported): in registers, or for many experts per lane in shared memory
     constexpr bool KEEP_BIAS = EPL <= 8;
     float bias[KEEP_BIAS ? EPL : 1];
+    __shared__ float4 s_bias[KEEP_BIAS ? 1 : EPL / 4 * LPT];   // experts 4 q .. 4 q + 3 of a lane at [q LPT + lane]
     grid_wait();
     grid_launch_next();
     float bmax = 0.0f;                           // of the finite biases
-    if (p.bias) {
+    {
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const float b = i < cnt ? __ldg(p.bias + e0 + i) : 0.0f;
-            if (KEEP_BIAS) bias[KEEP_BIAS ? i : 0] = b < INFINITY ? b : -INFINITY;
-            if (fabsf(b) < INFINITY) bmax = fmaxf(bmax, fabsf(b));
+            float b = p.bias && i < cnt ? __ldg(p.bias + e0 + i) : 0.0f;
             bad |= !(b < INFINITY);
+            b = b < INFINITY ? b : -INFINITY;
+            if (b > -INFINITY) bmax = fmaxf(bmax, fabsf(b));
+            if (KEEP_BIAS) bias[KEEP_BIAS ? i : 0] = b;
+            else if (warp == 0 && half == 0) reinterpret_cast<float*>(&s_bias[(i >> 2) * LPT + lane])[i & 3] = b;
         }
-        bmax = __int_as_float(__reduce_max_sync(all, __float_as_int(bmax)));
+        bmax = __int_as_float(__reduce_max_sync(all, __float_as_int(bmax)));   // every half has all experts
         if (bad) record_error(-7 /* MOE_ERR_CHECK */);
-    } else if (KEEP_BIAS) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) bias[KEEP_BIAS ? i : 0] = 0.0f;
+        if (!KEEP_BIAS) __syncthreads();
     }
-    const long long stride = (long long)gridDim.x * ROUTE_WARPS;
-    long long t = (long long)blockIdx.x * ROUTE_WARPS + warp;
+    const long long stride = (long long)gridDim.x * ROUTE_WARPS * TOKENS;
+    long long t0 = ((long long)blockIdx.x * ROUTE_WARPS + warp) * TOKENS;      // the warp's first token
     float l[EPL];
     auto load = [&](long long tok) {
         const float* row = p.logits + tok * p.E;
+        const int cnt = tok < p.T ? at.cnt : 0;               // a half without a token: every expert masked
         if (VEC) {
 #pragma unroll
             for (int i = 0; i < EPL; i += 4) {
@@ -328,8 +362,9 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 4 : 1) route_scor
             }
         }
     };
-    if (t < p.T) load(t);
-    for (; t < p.T; t += stride) {
+    if (t0 < p.T) load(t0 + half);
+    for (; t0 < p.T; t0 += stride) {
+        const long long t = t0 + half;
         const float* row = p.logits + t * p.E;
         // ---- keys
         bool bad = false;
@@ -339,12 +374,12 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 4 : 1) route_scor
             bad |= !(l[i] < INFINITY);
             l[i] = l[i] < INFINITY ? l[i] : -INFINITY;
         }
-        if (__any_sync(all, bad) && lane == 0) record_error(-7 /* MOE_ERR_CHECK */);
+        if (__any_sync(all, bad) && threadIdx.x % 32 == 0) record_error(-7 /* MOE_ERR_CHECK */);
         float ex[EPL];                                        // e^(l - top) or e^-l
         if (KIND == ROUTE_SOFTMAX || (KIND == ROUTE_LOGIT && !p.sigmoid && !p.renorm)) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) top = fmaxf(top, l[i]);
-            top = from_ordered(__reduce_max_sync(all, ordered(top + 0.0f)));
+            top = from_ordered(lanes_max<LPT>(ordered(top + 0.0f)));
             const float ref = top > -INFINITY ? top : 0.0f;
             float part_sum = 0.0f;
 #pragma unroll
@@ -352,26 +387,30 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 4 : 1) route_scor
                 ex[i] = exp_approx(l[i] - ref);               // 0 for -inf
                 part_sum += ex[i];
             }
-            total = warp_sum(part_sum);
+            total = lanes_sum<LPT>(part_sum);
             inv = 1.0f / total;
         }
         int key[EPL];
+        constexpr int Q = EPL < 4 ? EPL : 4;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            float k32 = l[i];
-            if (KIND != ROUTE_LOGIT) {
-                float b = 0.0f;
-                if (KEEP_BIAS) b = bias[KEEP_BIAS ? i : 0];
-                else if (p.bias && i < cnt) {
-                    b = __ldg(p.bias + e0 + i);
-                    b = b < INFINITY ? b : -INFINITY;
-                }
-                const float s = KIND == ROUTE_SIGMOID ? rcp_approx(1.0f + exp_approx(-l[i])) : ex[i] * inv;
-                k32 = l[i] > -INFINITY ? s + b : -INFINITY;
+        for (int q = 0; q < EPL; q += Q) {
+            float b4[4];
+            if (!KEEP_BIAS && KIND != ROUTE_LOGIT) {
+                const float4 v = s_bias[(q >> 2) * LPT + lane];
+                b4[0] = v.x; b4[1] = v.y; b4[2] = v.z; b4[3] = v.w;
             }
-            key[i] = (ordered(k32 + 0.0f) & ~POS) | (POS - i);
+#pragma unroll
+            for (int r = 0; r < Q; ++r) {
+                const int i = q + r;
+                float k32 = l[i];
+                if (KIND != ROUTE_LOGIT) {
+                    const float s = KIND == ROUTE_SIGMOID ? rcp_approx(1.0f + exp_approx(-l[i])) : ex[i] * inv;
+                    k32 = l[i] > -INFINITY ? s + (KEEP_BIAS ? bias[KEEP_BIAS ? i : 0] : b4[r]) : -INFINITY;
+                }
+                key[i] = (ordered(k32 + 0.0f) & ~POS) | (POS - i);
+            }
         }
-        if (t + stride < p.T) load(t + stride);               // on its way while this token is finished
+        if (t0 + stride < p.T) load(t + stride);              // on its way while this token is finished
         int head[D];
         largest<EPL, D>(key, 0x7fffffff, head);
         bool sure = true;
@@ -392,41 +431,42 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 4 : 1) route_scor
             bool kept = false;
             int lo = ORD_EMPTY;
             for (int q = 0; q < p.topk_group; ++q) {
-                const int most = __reduce_max_sync(all, v);
-                if (most == ORD_EMPTY) break;
-                lo = most;
-                const int owner = __ffs(__ballot_sync(all, v == most)) - 1;
-                if (g == (owner >> m.lg)) {
+                const int most = lanes_max<LPT>(v);
+                lo = most != ORD_EMPTY ? most : lo;
+                const int owner = __ffs(lanes_ballot<LPT>(v == most)) - 1;
+                if (g == (owner >> m.lg) && most != ORD_EMPTY) {
                     kept = true;
                     v = ORD_EMPTY;
                 }
             }
-            const int hi = __reduce_max_sync(all, v);
+            const int hi = lanes_max<LPT>(v);
             if (hi != ORD_EMPTY) {
                 const float fl = from_ordered(lo), fh = from_ordered(hi);
-                // a value is one key, or two: each within the error of a key of twice its size
-                sure = KIND == ROUTE_LOGIT ? lo > hi
-                                           : fl - fh > 2.0f * (route_err_any(p.sigmoid, 2.0f * fl, bmax) +
-                                                               route_err_any(p.sigmoid, 2.0f * fh, bmax)) +
-                                                           4.0f * TRUNC * (fabsf(fl) + fabsf(fh) + bmax);
+                if (KIND == ROUTE_LOGIT) {
+                    sure = lo > hi;
+                } else {      // a value is one key, or two of at most |value| + bmax each
+                    constexpr bool SIG = KIND == ROUTE_SIGMOID;
+                    const float two = p.top2 ? 2.0f : 1.0f, more = p.top2 ? bmax : 0.0f;
+                    const float kl = fabsf(fl) + more, kh = fabsf(fh) + more;
+                    sure = fl - fh > two * (route_err_any(SIG, kl, bmax) + route_err_any(SIG, kh, bmax) + TRUNC * (kl + kh)) +
+                                         2.4e-7f * (fabsf(fl) + fabsf(fh));
+                }
             }
             if (!kept) {
 #pragma unroll
                 for (int i = 0; i < D; ++i) head[i] = ORD_EMPTY;
             }
         }
-        // ---- slots: lane j takes the j-th largest key and the lanes it was on (more than one: keys that agree but
-        // for what 64 bits will tell); lane k (k = 32: `next`) the one after the last slot
-        int mine = ORD_EMPTY, next = ORD_EMPTY;
-        unsigned from = 0;
+        // ---- slots: lane j takes the j-th largest key and its lane; lane k (k < LPT) the one that comes next
+        const int last = min(p.k, LPT - 1);
+        int mine = ORD_EMPTY, from = 0;
 #pragma unroll 1
-        for (int j = 0; j <= p.k; ++j) {                      // past the last unmasked key: keys below ORD_LOWEST
-            const int hi = __reduce_max_sync(all, head[0]);
-            const bool taken = head[0] == hi;
-            const unsigned on = __ballot_sync(all, taken);
+        for (int j = 0; j <= last; ++j) {                     // past the last unmasked key: keys below ORD_LOWEST
+            const int hi = lanes_max<LPT>(head[0]);
+            const int owner = __ffs(lanes_ballot<LPT>(head[0] == hi)) - 1;
+            const bool taken = lane == owner;
             mine = lane == j ? hi : mine;
-            from = lane == j ? on : from;
-            if (j == MAX_TOPK) next = hi;
+            from = lane == j ? owner : from;
 #pragma unroll
             for (int i = 0; i + 1 < D; ++i) head[i] = taken ? head[i + 1] : head[i];
             head[D - 1] = taken ? ORD_EMPTY : head[D - 1];
@@ -434,32 +474,88 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, EPL <= 8 ? 4 : 1) route_scor
                 if (taken) largest<EPL, D>(key, hi, head);
             }
         }
-        sure = sure && (mine < ORD_LOWEST || (from & (from - 1)) == 0);
+        const bool entry = lane <= last && mine >= ORD_LOWEST;
         int my_e = -1;
         float my_l = 0.0f;
-        if (mine >= ORD_LOWEST) {
-            const int q = __ffs(from) - 1;
-            my_e = (q >> m.lg) * m.each + (q & ((1 << m.lg) - 1)) * m.per + (POS - (mine & POS));
+        if (entry) {
+            my_e = (from >> m.lg) * m.each + (from & ((1 << m.lg) - 1)) * m.per + (POS - (mine & POS));
             my_l = scored_logit(p, row, my_e);
         }
-        // ---- is the order certain?
-        int after = __shfl_down_sync(all, mine, 1);
-        if (lane == 31) after = next;
-        const bool pair = lane < p.k && after >= ORD_LOWEST;
-        if (KIND == ROUTE_LOGIT) {
-            if (pair) sure = sure && (mine | POS) > (after | POS);
-        } else {
-            const float ka = from_ordered(mine & ~POS), kb = from_ordered(after & ~POS);
-            constexpr bool SIG = KIND == ROUTE_SIGMOID;
+        // ---- is the order certain?  Slot j against slot j + 1, by their whole keys, and every slot against `rest`, the
+        // most that any other key can be
+        const int next = p.k < LPT ? __shfl_sync(all, mine, p.k & (LPT - 1), LPT) : lanes_max<LPT>(head[0]);
+        const float rest = from_ordered(next | POS);
+        constexpr bool SIG = KIND == ROUTE_SIGMOID;
+        float ka = my_l, ea = 0.0f;
+        if (KIND != ROUTE_LOGIT) {
             const float x = SIG ? my_l : my_l - top;
             const float s = SIG ? rcp_approx(1.0f + exp_approx(-x)) : exp_approx(x) * inv;
-            const float ea = route_err(SIG, s, x, ka);
-            float eb = __shfl_down_sync(all, ea, 1);
-            if (lane == 31) eb = route_err_any(SIG, kb, bmax);
-            if (pair) sure = sure && ka - kb > ea + eb + TRUNC * (fabsf(ka) + fabsf(kb));
+            ka = s + (p.bias && entry ? __ldg(p.bias + my_e) : 0.0f);
+            ea = route_err(SIG, s, x, ka);
         }
-        if (__all_sync(all, sure)) scored_weights(p, t, lane, my_e, my_l, top, total);
-        else route_token_f64(p, m, t, lane, route_keys + (size_t)warp * 32 * m.per);
+        const float kb = __shfl_down_sync(all, ka, 1), eb = __shfl_down_sync(all, ea, 1);
+        const int after = __shfl_down_sync(all, mine, 1);
+        bool order = true;
+        if (entry && lane < p.k) {
+            // equal logits of two lanes may have come in the order of their positions
+            if (lane + 1 < p.k && after >= ORD_LOWEST) order = ka - kb > ea + eb;
+            if (next >= ORD_LOWEST)
+                sure = sure && (KIND == ROUTE_LOGIT ? ka > rest : ka - rest > ea + route_err_any(SIG, rest, bmax));
+        }
+        // The slots are the right experts if all are certainly above the rest; otherwise, and where the groups were in
+        // doubt, the token is done again.  Their order among themselves is put right here.
+        const unsigned certain = lanes_ballot<LPT>(order);
+        const unsigned doubt = ~certain & (p.k < 32 ? (1u << p.k) - 1u : all);
+        if (__any_sync(all, doubt != 0)) {
+            double t64 = 1.0;
+            if (KIND == ROUTE_SOFTMAX) {
+                double part_sum = 0.0;
+                if (t < p.T) {
+#pragma unroll 2
+                    for (int i = 0; i < cnt; ++i) {
+                        const float v = scored_logit(p, row, e0 + i);
+                        part_sum += v < INFINITY && v > -INFINITY ? exp((double)v - (double)top) : 0.0;
+                    }
+                }
+#pragma unroll
+                for (int o = LPT / 2; o > 0; o >>= 1) part_sum += __shfl_xor_sync(all, part_sum, o);
+                t64 = part_sum;
+            }
+            double k64 = my_l;
+            if (KIND != ROUTE_LOGIT && entry)
+                k64 = (KIND == ROUTE_SIGMOID ? 1.0 / (1.0 + exp(-(double)my_l)) : exp((double)my_l - (double)top) / t64) +
+                      (double)(p.bias ? __ldg(p.bias + my_e) : 0.0f);
+            if (!entry) k64 = -INFINITY;
+            int rank = 0;
+            for (int j = 0; j <= last; ++j) {                 // this entry's place among the entries
+                const double o = __shfl_sync(all, k64, j, LPT);
+                const int oe = __shfl_sync(all, my_e, j, LPT);
+                rank += o > k64 || (o == k64 && oe < my_e);
+            }
+            int e2 = -1;
+            float l2 = 0.0f;
+            for (int j = 0; j <= last; ++j) {
+                const int r = __shfl_sync(all, entry ? rank : LPT, j, LPT), oe = __shfl_sync(all, my_e, j, LPT);
+                const float ol = __shfl_sync(all, my_l, j, LPT);
+                if (r == lane) {
+                    e2 = oe;
+                    l2 = ol;
+                }
+            }
+            my_e = e2;
+            my_l = l2;
+        }
+        const unsigned unsure = __ballot_sync(all, !sure && t < p.T);
+        scored_weights<LPT>(p, t, t < p.T && (LPT == 32 ? unsure == 0 : (unsure >> (16 * half) & 0xffffu) == 0), lane, my_e,
+                            my_l, top, total);
+        if (unsure) {
+            if (unsure & (LPT == 32 ? all : 0xffffu))
+                route_token_f64(p, m64, t0, threadIdx.x & 31, route_keys + (size_t)warp * 32 * m64.per);
+            if (LPT == 16 && unsure >> 16) {
+                __syncwarp();
+                route_token_f64(p, m64, t0 + 1, threadIdx.x & 31, route_keys + (size_t)warp * 32 * m64.per);
+            }
+        }
     }
 }
 

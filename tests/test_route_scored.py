@@ -91,9 +91,8 @@ def check(moe, logits, bias, k, **kw):
     idx, w = call(moe, logits, bias, k, **kw)
     ri, rw = define(logits, bias, k, **kw)
     assert np.array_equal(idx, ri)
-    fin = np.where(np.isfinite(logits), logits, np.nan)
-    span = np.nan_to_num(np.nanmax(np.where(np.isfinite(fin), fin, -3e38), axis=1) -
-                         np.nanmin(np.where(np.isfinite(fin), fin, 3e38), axis=1))
+    live = np.isfinite(logits)
+    span = np.where(live, logits, -3e38).max(1).astype(np.float64) - np.where(live, logits, 3e38).min(1)
     tol = (np.clip(span, 0, 1e3) + 64) * 2.0 ** -24
     assert (np.abs(w - rw) <= tol[:, None] * np.abs(rw) + 1e-37).all()
     return idx, w
@@ -204,6 +203,28 @@ def test_values(moe, T, E, k, n_group, topk_group, sigmoid, with_bias):
 def test_many_tokens(moe):
     check(moe, draw(20011, 96, 5), draw_bias(96, 5), 6, n_group=6, topk_group=3, scale=2.5)
     check(moe, draw(9001, 256, 6), draw_bias(256, 6), 8, n_group=8, topk_group=4, scale=2.5)
+    assert moe.moe_get_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("E,k,n_group,topk_group", [(8, 2, 1, 1), (16, 15, 1, 1), (60, 6, 1, 1), (72, 5, 12, 4),
+                                                    (128, 8, 1, 1), (130, 9, 1, 1), (187, 1, 1, 1), (256, 15, 16, 7),
+                                                    (240, 8, 15, 2), (64, 16, 8, 4)])
+def test_many_tokens_of_every_kind(moe, E, k, n_group, topk_group):
+    # enough tokens for two per warp where that is done; an odd number, a masked tail, near and exact ties
+    T = 4999
+    logits = draw(T, E, E)
+    logits[::7] = np.round(logits[::7] * 2) / 2
+    r = np.random.default_rng(E)
+    near = np.stack([r.permutation(E) for _ in range(len(logits[3::11]))]).astype(np.int32)
+    logits[3::11] = (logits[3::11, :1].view(np.int32) + near).view(np.float32)
+    logits[5::13][r.random(logits[5::13].shape) < 0.7] = -np.inf
+    logits[-31:] = -np.inf
+    kw = dict(n_group=n_group, topk_group=topk_group)
+    check(moe, logits, draw_bias(E, 8), k, top2=True, sigmoid=True, scale=2.5, **kw)
+    check(moe, logits, draw_bias(E, 8, 1.0 / E), k, top2=False, sigmoid=False, renorm=False, **kw)
+    check(moe, logits, None, k, top2=False, sigmoid=False, **kw)
+    check(moe, logits, np.zeros(E, np.float32), k, top2=True, sigmoid=True, renorm=False, **kw)
     assert moe.moe_get_error() == 0
 
 
