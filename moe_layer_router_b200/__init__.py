@@ -6,7 +6,8 @@ torch stream, and turns a non-zero status into ``MoeError``.  There is no CPU
 fallback: if the library is missing, importing the binding raises.
 
 Names follow the C ABI: ``moe_route``, ``moe_permute``, ``moe_expert_ffn``,
-``moe_combine``, ``moe_layer_forward``, plus the helpers ``moe_capacity``,
+``moe_combine``, ``moe_layer_forward``, the scored router ``moe_route_scored`` and its layers
+``moe_layer_forward_scored[_w8]``, the dense layer ``moe_linear[_w8a8]``, plus the helpers ``moe_capacity``,
 ``moe_workspace_bytes``, ``moe_workspace_layout``, ``moe_get_error``,
 ``moe_strerror``.  Tensors are torch tensors (bf16 / fp32 / int32, contiguous);
 ``None`` passes NULL.
@@ -200,6 +201,20 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _here(*tensors) -> None:
+    """The kernels run on the current device: refuse tensors of another one (or of the host)."""
+    dev = None
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        d = t.get_device()
+        if d >= 0 and dev is None:
+            import torch
+            dev = torch.cuda.current_device()
+        if d != dev:
+            raise ValueError(f"a tensor is on {t.device}, not on the current device")
+
+
 try:
     from torch._C import _cuda_getCurrentRawStream as _raw_stream
 except ImportError:      # a torch build without it
@@ -247,6 +262,7 @@ def moe_route(x, Wg, bias, logits_in, T, d, E, k, logits_out, idx, w, ws, stream
 
 def moe_route_scored(x, Wg, bias, logits_in, params: moe_route_params, T, d, E, k, logits_out, idx, w, ws,
                      stream=None) -> None:
+    _here(x, Wg, bias, logits_in, logits_out, idx, w, ws)
     _check(_lib.moe_route_scored(_ptr(x), _ptr(Wg), _ptr(bias), _ptr(logits_in),
                                  ctypes.byref(params) if params is not None else None, T, d, E, k, _ptr(logits_out),
                                  _ptr(idx), _ptr(w), _ptr(ws), _nbytes(ws), _stream(stream)), "moe_route_scored")
@@ -290,6 +306,7 @@ def moe_layer_forward(x, Wg, bias, W1, W3, W2, W1s, W3s, W2s, f_shared, T, d, E,
 
 def moe_layer_forward_scored(x, Wg, bias, params: moe_route_params, W1, W3, W2, W1s, W3s, W2s, f_shared, T, d, E, k, f,
                              capacity_factor, cap_mode, out, ws, stream=None) -> None:
+    _here(x, Wg, bias, W1, W3, W2, W1s, W3s, W2s, out, ws)
     _check(_lib.moe_layer_forward_scored(_ptr(x), _ptr(Wg), _ptr(bias),
                                          ctypes.byref(params) if params is not None else None, _ptr(W1), _ptr(W3),
                                          _ptr(W2), _ptr(W1s), _ptr(W3s), _ptr(W2s), f_shared, T, d, E, k, f,
@@ -301,6 +318,7 @@ def moe_layer_forward_scored_w8(x, Wg, bias, params: moe_route_params, routed: d
                                 activations_fp8, T, d, E, k, f, capacity_factor, cap_mode, out, ws,
                                 stream=None) -> None:
     """routed / shared: dicts of W1q, W3q, W2q, s1, s3, s2 tensors (shared None without a shared expert)."""
+    _here(x, Wg, bias, out, ws, *routed.values(), *(shared or {}).values())
     q, qs = _w8(routed), _w8(shared)
     _check(_lib.moe_layer_forward_scored_w8(_ptr(x), _ptr(Wg), _ptr(bias),
                                             ctypes.byref(params) if params is not None else None, ctypes.byref(q),
@@ -312,6 +330,7 @@ def moe_layer_forward_scored_w8(x, Wg, bias, params: moe_route_params, routed: d
 
 def moe_layer_route_count_scored(x, Wg, bias, params: moe_route_params, f_shared, T, d, E, k, f, ws,
                                  stream=None) -> None:
+    _here(x, Wg, bias, ws)
     _check(_lib.moe_layer_route_count_scored(_ptr(x), _ptr(Wg), _ptr(bias),
                                              ctypes.byref(params) if params is not None else None, f_shared, T, d, E,
                                              k, f, _ptr(ws), _nbytes(ws), _stream(stream)),
@@ -320,6 +339,7 @@ def moe_layer_route_count_scored(x, Wg, bias, params: moe_route_params, f_shared
 
 def moe_linear(x, W, W_up, bias, bias_up, residual, M, N, K, act, y, stream=None) -> None:
     """y = act(x W^T + bias) + residual; act MOE_ACT_SWIGLU takes W_up (and bias_up), the others None."""
+    _here(x, W, W_up, bias, bias_up, residual, y)
     _check(_lib.moe_linear(_ptr(x), _ptr(W), _ptr(W_up), _ptr(bias), _ptr(bias_up), _ptr(residual), M, N, K, act,
                            _ptr(y), _stream(stream)), "moe_linear")
 
@@ -332,6 +352,7 @@ def moe_linear_workspace_bytes(M: int, K: int) -> int:
 
 def moe_linear_w8a8(x, Wq, s, Wq_up, s_up, bias, bias_up, residual, M, N, K, act, y, ws, stream=None) -> None:
     """moe_linear with e4m3 weight bytes and one fp32 scale per weight row; x is quantised row by row into ws."""
+    _here(x, Wq, s, Wq_up, s_up, bias, bias_up, residual, y, ws)
     _check(_lib.moe_linear_w8a8(_ptr(x), _ptr(Wq), _ptr(s), _ptr(Wq_up), _ptr(s_up), _ptr(bias), _ptr(bias_up),
                                 _ptr(residual), M, N, K, act, _ptr(y), _ptr(ws), _nbytes(ws), _stream(stream)),
            "moe_linear_w8a8")

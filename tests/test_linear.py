@@ -123,9 +123,11 @@ def test_refusals(moe):
     for M, K in [(0, 64), (8, 40), (8, 0)]:
         with pytest.raises(moe.MoeError):
             moe.moe_linear_workspace_bytes(M, K)
-    with pytest.raises(ValueError):
-        moe.moe_linear(torch.zeros(64, 8, dtype=torch.bfloat16).t(), 16, None, None, None, None, 8, 64, 64, 0, 64,
-                       stream=0)
+    host = torch.zeros(8, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="cpu"):          # host tensors are refused before they reach a kernel
+        moe.moe_linear(host, 16, None, None, None, None, 8, 64, 64, 0, 64, stream=0)
+    with pytest.raises(ValueError, match="cpu"):
+        moe.moe_linear_w8a8(16, host, 32, None, None, None, None, None, 8, 64, 64, 0, 64, 128, stream=0)
 
 
 def test_definition_gelu_forms_agree_with_their_formulas():
@@ -204,6 +206,14 @@ def test_residual_in_place_and_repeatable(moe, M, N, K):
     inplace = a["residual"].clone()
     moe.moe_linear(a["x"], a["W"], None, a["bias"], None, inplace, M, N, K, 0, inplace)
     assert torch.equal(inplace, y)
+
+
+@gpu
+def test_transposed_tensors_are_refused(moe):
+    a = inputs(16, 64, 64, "none", False, False)
+    y = torch.zeros(64, 16, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        moe.moe_linear(a["x"], a["W"], None, None, None, None, 16, 64, 64, 0, y.t())
 
 
 @gpu

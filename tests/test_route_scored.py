@@ -136,8 +136,8 @@ def test_refusals(moe):
     assert _raw(moe, logits=None, x=16, Wg=16, d=100) == shape
     assert _raw(moe, logits=None, x=16, Wg=24, d=64) == align
     assert _raw(moe, logits=None, x=16, Wg=16, d=64, ws=16, nws=100) == small
-    with pytest.raises(ValueError):
-        moe.moe_route_scored(None, None, None, torch.zeros(8, 64).t(), P(), 64, 64, 8, 2, None, 16, 16, None, stream=0)
+    with pytest.raises(ValueError, match="cpu"):          # host tensors are refused before they reach a kernel
+        moe.moe_route_scored(None, None, None, torch.zeros(8, 64), P(), 8, 64, 64, 2, None, 16, 16, None, stream=0)
 
 
 def test_layer_refusals(moe):
