@@ -543,8 +543,10 @@ linear_rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ W, con
 // stages and two accumulators, so that a tile's epilogue runs under the next tile's products.
 // The last token tile runs its MMAs with N = its tokens rounded up to 16.
 constexpr int LINP_MAX_STAGES = 10;
-constexpr int LINP_EPI_BYTES = 8 * 2 * 2048;                       // two 2 KB buffers per epilogue warp
-constexpr int LINP_THREADS = 320;                                  // TMA, MMA, 8 epilogue warps
+// 8 epilogue warps that finish 32 tokens at a time, or 16 and 16: with more warps a step's waits cost less, but rows
+// are moved in smaller pieces.  By K (see launch_linear_pair).
+__host__ __device__ constexpr int linear_pair_threads(int warps) { return 64 + 32 * warps; }
+constexpr int LINP_EPI_BYTES = 2 * 16384;                          // two buffers per epilogue warp
 constexpr int LINP_SMEM_BYTES = GEMM_SMEM_MAX;
 // 128 weight rows and half of the tile's tokens; 6 stages at 256 tokens, 10 at 32
 __host__ __device__ constexpr int linear_pair_stage_bytes(int bn) { return LIN_A_BYTES + bn / 2 * 128; }
@@ -571,15 +573,22 @@ __device__ __forceinline__ LinearTile linear_tile(const LinearParams& p, int t, 
     return r;
 }
 
-// Accumulator fragments: 16 tensor-memory lanes x 32 columns.  v[4 i], v[4 i + 1]: lane l / 4, columns
+// Accumulator fragments: 16 tensor-memory lanes x CH columns (32 or 16).  v[4 i], v[4 i + 1]: lane l / 4, columns
 // 8 i + 2 (l % 4), + 1; v[4 i + 2], v[4 i + 3]: lane l / 4 + 8, the same columns (l: this thread's lane).
-__device__ __forceinline__ void tmem_ld_frag16x32(uint32_t taddr, uint32_t* v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr));
+template <int CH>
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t* v) {
+    static_assert(CH == 32 || CH == 16, "");
+    if constexpr (CH == 32)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+              "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+            : "r"(taddr));
+    else
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "r"(taddr));
 }
 __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&r)[4]) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
@@ -594,18 +603,18 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
 }
 
 // One epilogue warp's 32 accumulator lanes of a tile.  The accumulator is read as 8 x 8 fragments (rows: outputs,
-// columns: tokens), finished in registers, and transposed by stmatrix into 2 KB of shared memory as token rows
+// columns: tokens), finished in registers, and transposed by stmatrix into shared memory as token rows
 // of 64 bytes, from which 16-byte pieces of whole rows go to y; the residual comes in the other way.  Per 8
 // outputs that is 4 conversions, one shared-memory instruction each way and an eighth of a global store; with a lane
 // per output each of these was 8 instructions (16384 x 2048 x 512 with residual: 61 us this way, 68 us a lane per
 // output, 105 us through fp32 [token][output] in shared memory).  Pieces are XOR-swizzled by row: no bank conflicts.
 // Rows of y that are not 16-byte aligned (N % 8) are moved an element per lane.
 // GATED: lanes 0-63 of the CTA's accumulator hold x W^T, lanes 64-127 x W_up^T of the same 64 outputs.  The two
-// warps of a pair swap halves of every 32 tokens (through the other's 2 KB, two of them in turn) and each finishes
-// 16 tokens.
-template <bool F8, bool GATED>
+// warps of a pair swap halves of every CH tokens (through the other's buffer, two of them in turn) and each finishes
+// one half.
+template <bool F8, bool GATED, int CH>
 struct LinearWarp {
-    static constexpr int NB = GATED ? 2 : 4;   // blocks of 8 tokens that this warp finishes, of the chunk's 4
+    static constexpr int NB = GATED ? CH / 16 : CH / 8;   // blocks of 8 tokens that this warp finishes, of the chunk's CH / 8
     float bias[4], sw[4];     // of outputs l / 4 + 8 b, b = 0..3
     int n, nvalid;            // first output; how many of the 32 exist
     int own;                  // first of this warp's tokens in a chunk
@@ -615,7 +624,7 @@ struct LinearWarp {
     __device__ __forceinline__ void begin(const LinearParams& p, int first, bool up, int lane) {
         n = first;
         nvalid = max(0, min(32, p.N - first));
-        own = up ? 16 : 0;
+        own = up ? CH / 2 : 0;
         vec = (p.N & 7) == 0;
         const float* bp = up ? p.bias_up : p.bias;
         const float* sp = up ? p.sw_up : p.sw;
@@ -648,38 +657,34 @@ struct LinearWarp {
                 const int r = 8 * j + (lane >> 2);
                 reinterpret_cast<uint4*>(mine)[r * 4 + (q ^ ((r >> 1) & 3))] = rr[j];
             }
-            load_residual(p, token + 32, cnt_next, lane);
-        } else if (nvalid > 0 && rows > 0) {      // 16 loads at a time; masked ones repeat the last element
+            load_residual(p, token + CH, cnt_next, lane);
+        } else if (nvalid > 0 && rows > 0) {      // all loads at once; masked ones repeat the last element
             const unsigned short* src = reinterpret_cast<const unsigned short*>(p.residual) + (token + own) * p.N + n +
                                         min(lane, nvalid - 1);
-#pragma unroll 1
-            for (int r0 = 0; r0 < 8 * NB; r0 += 16) {
-                unsigned short u[16];
+            unsigned short u[8 * NB];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) u[r] = src[(long long)min(r0 + r, rows - 1) * p.N];
+            for (int r = 0; r < 8 * NB; ++r) u[r] = src[(long long)min(r, rows - 1) * p.N];
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    reinterpret_cast<unsigned short*>(mine)[(r0 + r) * 32 + (((lane >> 3) ^ ((r >> 1) & 3)) << 3) +
-                                                            (lane & 7)] = u[r];
-            }
+            for (int r = 0; r < 8 * NB; ++r)
+                reinterpret_cast<unsigned short*>(mine)[r * 32 + (((lane >> 3) ^ ((r >> 1) & 3)) << 3) + (lane & 7)] = u[r];
         }
     }
-    // tokens [token, token + cnt), 1 <= cnt <= 32, from the accumulator at taddr; cnt_next: tokens after them.
-    // mine / other: 2 KB of this warp / of its partner; bar: the pair's barrier; VEC: `vec`
+    // tokens [token, token + cnt), 1 <= cnt <= CH, from the accumulator at taddr; cnt_next: tokens after them.
+    // mine / other: 64 CH bytes of this warp / of its partner; bar: the pair's barrier; VEC: `vec`
     template <bool VEC>
     __device__ __forceinline__ void chunk(const LinearParams& p, uint32_t taddr, long long token, int cnt, int cnt_next,
                                           int lane, uint8_t* mine, uint8_t* other, int bar) {
-        uint32_t v[32];
+        uint32_t v[CH];
         __syncwarp();
-        tmem_ld_frag16x32(taddr, v);
-        tmem_ld_frag16x32(taddr + (16u << 16), v + 16);
+        tmem_ld_frag<CH>(taddr, v);
+        tmem_ld_frag<CH>(taddr + (16u << 16), v + CH / 2);
         const int q = lane & 3;
         const int rows = min(cnt - own, 8 * NB);             // of this warp's tokens (may be <= 0)
         if (!GATED && p.residual) stage_residual<VEC>(p, token, rows, cnt_next, lane, mine);
         tmem_ld_wait();
-        float z[32];                                          // [8 i + 2 b + h]: token 8 i + 2 (l % 4) + h, output block b
+        float z[CH];                                          // [8 i + 2 b + h]: token 8 i + 2 (l % 4) + h, output block b
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < CH / 8; ++i) {
             float2 sx = make_float2(1.0f, 1.0f);
             if (F8) {
                 const int tok = 8 * i + 2 * (lane & 3);
@@ -690,34 +695,34 @@ struct LinearWarp {
             for (int b = 0; b < 4; ++b)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float a = __uint_as_float(v[16 * (b >> 1) + 4 * i + 2 * (b & 1) + h]);
+                    float a = __uint_as_float(v[CH / 2 * (b >> 1) + 4 * i + 2 * (b & 1) + h]);
                     if (F8) a *= (h ? sx.y : sx.x) * sw[b];
                     z[8 * i + 2 * b + h] = a + bias[b];
                 }
         }
         float o[8 * NB];
         if (GATED) {
-            // the partner's 16 tokens go to it, this warp's come from it
+            // the partner's half of the tokens goes to it, this warp's comes from it
             float4* out = reinterpret_cast<float4*>(other) + lane;
             const float4* in = reinterpret_cast<const float4*>(mine) + lane;
             const bool up = own != 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < CH / 8; ++j) {
                 float4 w;
-                w.x = up ? z[4 * j] : z[16 + 4 * j];
-                w.y = up ? z[4 * j + 1] : z[16 + 4 * j + 1];
-                w.z = up ? z[4 * j + 2] : z[16 + 4 * j + 2];
-                w.w = up ? z[4 * j + 3] : z[16 + 4 * j + 3];
+                w.x = up ? z[4 * j] : z[CH / 2 + 4 * j];
+                w.y = up ? z[4 * j + 1] : z[CH / 2 + 4 * j + 1];
+                w.z = up ? z[4 * j + 2] : z[CH / 2 + 4 * j + 2];
+                w.w = up ? z[4 * j + 3] : z[CH / 2 + 4 * j + 3];
                 out[32 * j] = w;
             }
             named_barrier(bar, 64);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < CH / 8; ++j) {
                 const float4 w = in[32 * j];
                 const float r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float m = up ? z[16 + 4 * j + e] : z[4 * j + e];
+                    const float m = up ? z[CH / 2 + 4 * j + e] : z[4 * j + e];
                     o[4 * j + e] = swiglu_f32(up ? r[e] : m, up ? m : r[e]);
                 }
             }
@@ -772,8 +777,8 @@ struct LinearWarp {
 };
 
 // Tensor maps as for linear_split_kernel, x with boxes of bn / 2 rows.
-template <bool F8, bool GATED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LINP_THREADS, 1)
+template <bool F8, bool GATED, int WARPS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(linear_pair_threads(WARPS), 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWup,
                    const __grid_constant__ CUtensorMap tmX, const __grid_constant__ LinearParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -807,7 +812,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull_bar + a, 1);
-            mbar_init(tempty_bar + a, 16);         // the epilogue warps of both CTAs
+            mbar_init(tempty_bar + a, 2 * WARPS);
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -901,27 +906,28 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             }
         }
     } else {
-        // each of the two warps of a lane quarter takes half of the tokens; GATED: quarters q and q + 2 are partners
-        const int sub = warp & 3, half = (warp - 2) >> 2;
+        // the WARPS / 4 warps of a lane quarter share the tokens; GATED: lane quarters q and q + 2 are partners
+        constexpr int CH = 256 / WARPS;                             // tokens of a step
+        const int sub = warp & 3, slot = (warp - 2) >> 2;
         const int part = GATED ? sub & 1 : sub;                     // 32 outputs of the CTA
         const bool up = GATED && sub >= 2;
-        const int bar = 1 + part + 2 * half;                        // GATED: the pair's barrier
+        const int bar = 1 + part + 2 * slot;                     // GATED: the pair's barrier
         const int tid = threadIdx.x - 64;
-        uint8_t* mine = rows + (sub + 4 * half) * 2048;             // 2 KB; the second set 16 KB further on
-        uint8_t* other = rows + ((sub ^ 2) + 4 * half) * 2048;
+        uint8_t* mine = rows + (sub + 4 * slot) * (64 * CH);       // the second set 16 KB further on
+        uint8_t* other = rows + ((sub ^ 2) + 4 * slot) * (64 * CH);
         const uint32_t tempty_leader = map_to_cta(tempty_bar, 0);
         int acc = 0;
         uint32_t acc_phase = 0, turn = 0;
         for (int t = pair; t < total; t += npairs) {
             const LinearTile ti = linear_tile(p, t, nt);
             const int n0 = (ti.n_idx * 2 + rank) * FT, nout = min(FT, p.N - n0);
-            const int share = (p.bn / 2 + 31) & ~31;                  // tokens of the first half
-            const int c0 = half * share, c1 = min(half ? p.bn : share, ti.ntok);
-            LinearWarp<F8, GATED> e;
+            const int share = (p.bn / (WARPS / 4) + CH - 1) / CH * CH;
+            const int c0 = slot * share, c1 = min(c0 + share, ti.ntok);
+            LinearWarp<F8, GATED, CH> e;
             e.begin(p, n0 + part * 32, up, lane);
             if (p.residual && e.vec && c0 < c1) e.load_residual(p, ti.t0 + c0, c1 - c0, lane);
             if (p.residual && nout > 0) {
-                for (int i = tid; i < ti.ntok * 3; i += 256) {       // a row's piece is at most 3 lines
+                for (int i = tid; i < ti.ntok * 3; i += 32 * WARPS) {   // a row's piece is at most 3 lines
                     const int tok = i / 3, col = min((i - tok * 3) * 64, nout - 1);
                     prefetch_l2(p.residual + (long long)(ti.t0 + tok) * p.N + n0 + col);
                 }
@@ -931,13 +937,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             if (!__all_sync(0xffffffffu, ready)) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + (uint32_t)(acc * GEMM_ACC_COLS) + ((uint32_t)(sub * 32) << 16);
-            for (int c = c0; c < c1; c += 32) {
+            for (int c = c0; c < c1; c += CH) {
                 const uint32_t set = (turn & 1u) * 16384u;
                 if (e.vec)
-                    e.template chunk<true>(p, tb + c, ti.t0 + c, min(32, c1 - c), c1 - c - 32, lane, mine + set,
+                    e.template chunk<true>(p, tb + c, ti.t0 + c, min(CH, c1 - c), c1 - c - CH, lane, mine + set,
                                            other + set, bar);
                 else
-                    e.template chunk<false>(p, tb + c, ti.t0 + c, min(32, c1 - c), c1 - c - 32, lane, mine + set,
+                    e.template chunk<false>(p, tb + c, ti.t0 + c, min(CH, c1 - c), c1 - c - CH, lane, mine + set,
                                             other + set, bar);
                 ++turn;
             }

@@ -1469,7 +1469,7 @@ int launch_linear_split(const LinearArgs& a, const LinearPlan& plan, cudaStream_
     return MOE_OK;
 }
 
-template <bool F8, bool GATED>
+template <bool F8, bool GATED, int WARPS>
 int launch_linear_pair(DeviceInfo* di, const LinearArgs& a, const LinearPlan& plan, cudaStream_t s) {
     LinearParams p = linear_params(a);
     const int nt = (a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
@@ -1482,10 +1482,11 @@ int launch_linear_pair(DeviceInfo* di, const LinearArgs& a, const LinearPlan& pl
     CUtensorMap mW, mWup, mX;
     int rc = linear_maps<F8, GATED>(a, p.bn / 2, &mW, &mWup, &mX);
     if (rc != MOE_OK) return rc;
-    if ((rc = opt_in_smem<linear_pair_kernel<F8, GATED>>()) != MOE_OK) return rc;
+    if ((rc = opt_in_smem<linear_pair_kernel<F8, GATED, WARPS>>()) != MOE_OK) return rc;
     cudaLaunchConfig_t cfg;
-    const LaunchAttrs attrs(&cfg, 2 * (unsigned)std::min(tiles, pairs), LINP_THREADS, LINP_SMEM_BYTES, s, 1);
-    if (cudaLaunchKernelEx(&cfg, linear_pair_kernel<F8, GATED>, mW, mWup, mX, p) != cudaSuccess) {
+    const LaunchAttrs attrs(&cfg, 2 * (unsigned)std::min(tiles, pairs), linear_pair_threads(WARPS),
+                            LINP_SMEM_BYTES, s, 1);
+    if (cudaLaunchKernelEx(&cfg, linear_pair_kernel<F8, GATED, WARPS>, mW, mWup, mX, p) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
@@ -1517,7 +1518,13 @@ int run_linear_as(DeviceInfo* di, const LinearArgs& a, cudaStream_t s) {
         if (a.M <= LINR_MAX_TOKENS) return launch_linear_rows<GATED>(a, s);
     }
     const LinearPlan plan = plan_linear(di->sms, a.M, a.N, a.K, F8, GATED, a.residual != nullptr);
-    return plan.pair ? launch_linear_pair<F8, GATED>(di, a, plan, s) : launch_linear_split<F8, GATED>(a, plan, s);
+    if (!plan.pair) return launch_linear_split<F8, GATED>(a, plan, s);
+    // A tile of short K is over before eight warps have finished the last one: 16 warps then (9407 x 10373 x 528
+    // with residual: 226 us with 8, 190 with 16; 16384 x 2048 x 512: 51.4, 49.1; 16384 x 4096 x 1024: 110, 117;
+    // 4096 x 14336 x 4096 gated: 638, 672).
+    const int nk = (a.K + (F8 ? 127 : 63)) / (F8 ? 128 : 64);
+    return nk <= 10 ? launch_linear_pair<F8, GATED, 16>(di, a, plan, s)
+                    : launch_linear_pair<F8, GATED, 8>(di, a, plan, s);
 }
 
 template <bool F8>
