@@ -19,7 +19,7 @@
 // token) to shared memory as fp32 [slice][token][128], each token's sums to the rank of the cluster that owns
 // the token, and each rank adds the slices of its tokens, applies the epilogue and stores.  What bounds it: the
 // weights' stream for few tokens (14336 x 4096, 16 tokens: 23.3 us, 5.0 of 6.46 TB/s), the operands' way from
-// L2 for hundreds (512 x 4096 x 4096: 25 us, 32 KB per 128 x 128 x 64 products at about 75 B per clock and SM);
+// L2 for hundreds (512 x 4096 x 4096: 23.5 us against the pairs' 18.6, 32 KB per 128 x 128 x 64 products);
 // setting up, handing over and joining take about 4 us besides.  Tried: pairs of CTAs (cta_group::2) in this
 // kernel, which halve the token traffic, won or lost under 10 % at 128 to 1024 tokens; prefetching weights into L2
 // ahead of the ring cost 5 to 20 %.
@@ -61,7 +61,7 @@ __host__ __device__ constexpr int linear_smem_bytes(int stages, int bn, int own_
 // Phi(-|z|) of the normal distribution: erfc(u) / 2 with u = |z| / sqrt(2) as t P(t) e^(-u^2) / 2, t = 1 / (1 + 0.4 u).
 // P is the degree-8 polynomial of least relative error against e^(u^2) erfc(u) / t on 0 < t <= 1 (1.3e-7, found by a
 // weighted least-squares iteration), halved here: the tail keeps its relative precision, at 20 instructions
-// where the library's erfc takes about twice as many (1152 x 7680 x 896: 45 us with that).
+// where the library's erfc takes about twice as many (1152 x 7680 x 896: 45 us with that, 25.5 with this).
 __device__ __forceinline__ float normal_tail(float z) {
     const float u = fabsf(z) * 0.70710678118654752f;
     const float t = __fdividef(1.0f, fmaf(0.4f, u, 1.0f));
@@ -228,21 +228,33 @@ __device__ __forceinline__ void linear_join(const LinearParams& p, const float* 
         if (f >= nout) return;
         const float ba = p.bias ? __ldg(p.bias + n) : 0.0f, bb = GATED && p.bias_up ? __ldg(p.bias_up + n) : 0.0f;
         const float wa = F8 ? __ldg(p.sw + n) : 1.0f, wb = F8 && GATED ? __ldg(p.sw_up + n) : 1.0f;
-#pragma unroll 4
-        for (int tok = tid / FT; tok < ntok; tok += STEP) {
-            const long long o = (t0 + tok) * p.N + n;
-            const float res = p.residual ? __bfloat162float(p.residual[o]) : 0.0f;
-            const float sx = F8 ? __ldg(p.sx + t0 + tok) : 1.0f;
-            float a = part[tok * LIN_BM + f], b = GATED ? part[tok * LIN_BM + 64 + f] : 0.0f;
+        constexpr int U = 8;                       // residuals fetched together: a store may alias the next load
+        for (int tok0 = tid / FT; tok0 < ntok; tok0 += U * STEP) {
+            float res[U];
 #pragma unroll
-            for (int r = 1; r < SPLIT; ++r) {
-                a += part[r * stride + tok * LIN_BM + f];
-                if (GATED) b += part[r * stride + tok * LIN_BM + 64 + f];
+            for (int u = 0; u < U; ++u) {
+                const int tok = tok0 + u * STEP;
+                res[u] = p.residual && tok < ntok ? __bfloat162float(p.residual[(t0 + tok) * p.N + n]) : 0.0f;
             }
-            if (F8) { a *= sx * wa; b *= sx * wb; }
-            a += ba;
-            a = GATED ? swiglu_f32(a, b + bb) : linear_act(p.act, a);
-            p.y[o] = __float2bfloat16_rn(p.residual ? a + res : a);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int tok = tok0 + u * STEP;
+                if (tok >= ntok) break;
+                float a = part[tok * LIN_BM + f], b = GATED ? part[tok * LIN_BM + 64 + f] : 0.0f;
+#pragma unroll
+                for (int r = 1; r < SPLIT; ++r) {
+                    a += part[r * stride + tok * LIN_BM + f];
+                    if (GATED) b += part[r * stride + tok * LIN_BM + 64 + f];
+                }
+                if (F8) {
+                    const float sx = __ldg(p.sx + t0 + tok);
+                    a *= sx * wa;
+                    b *= sx * wb;
+                }
+                a += ba;
+                a = GATED ? swiglu_f32(a, b + bb) : linear_act(p.act, a);
+                p.y[(t0 + tok) * p.N + n] = __float2bfloat16_rn(p.residual ? a + res[u] : a);
+            }
         }
     }
 }
@@ -602,12 +614,12 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                  : "memory");
 }
 
-// One epilogue warp's 32 accumulator lanes of a tile.  The accumulator is read as 8 x 8 fragments (rows: outputs,
+// One epilogue warp's 32 accumulator lanes of a tile, CH tokens at a time.  The accumulator is read as 8 x 8 fragments (rows: outputs,
 // columns: tokens), finished in registers, and transposed by stmatrix into shared memory as token rows
 // of 64 bytes, from which 16-byte pieces of whole rows go to y; the residual comes in the other way.  Per 8
 // outputs that is 4 conversions, one shared-memory instruction each way and an eighth of a global store; with a lane
-// per output each of these was 8 instructions (16384 x 2048 x 512 with residual: 61 us this way, 68 us a lane per
-// output, 105 us through fp32 [token][output] in shared memory).  Pieces are XOR-swizzled by row: no bank conflicts.
+// per output each of these was 8 instructions (16384 x 2048 x 512 with residual, as first built: 61 us this way,
+// 68 us a lane per output, 105 us through fp32 [token][output] in shared memory).  Pieces are XOR-swizzled by row: no bank conflicts.
 // Rows of y that are not 16-byte aligned (N % 8) are moved an element per lane.
 // GATED: lanes 0-63 of the CTA's accumulator hold x W^T, lanes 64-127 x W_up^T of the same 64 outputs.  The two
 // warps of a pair swap halves of every CH tokens (through the other's buffer, two of them in turn) and each finishes

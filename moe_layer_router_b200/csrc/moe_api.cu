@@ -455,7 +455,7 @@ int run_route_scored(DeviceInfo* di, const float* logits, int nsplit, float* log
     };
     const RouteLanes warp = lanes(32);
     // two tokens per warp once there are more of them than warps on the GPU at a time (measured: 32768 x 256, 8
-    // groups, 44 us with one, below with two)
+    // groups, 44 us with one, 38 with two)
     const bool two = k < 16 && r.n_group <= 16 && lanes(16).per <= 16 && T > 32ll * di->sms;
     const RouteLanes m = two ? lanes(16) : warp;
     const bool vec = nsplit == 1 && m.per % 4 == 0 && each % 4 == 0;
@@ -1386,15 +1386,16 @@ int linear_maps(const LinearArgs& a, int x_rows, CUtensorMap* mW, CUtensorMap* m
 //     the operands that pass into the busiest SM at 90 GB/s, 47 bytes per cycle (a tile's products, 2 bn cycles per
 //     k-block, take less);
 //   0.2 per wave of pair tiles; for `split` K slices 0.5 + 0.1 split + 0.026 bn, their hand-over and joining;
-//   where N is no multiple of 8, and rows are stored two bytes at a time, 0.02 bn for the last pair tile's
-//   outputs and 0.1 bn / split for each CTA of the split kernel, whose lanes each own a row.
+//   where rows are read and written an element at a time: pairs (N no multiple of 8) take 0.037 bn for a tile's outputs
+//   if its products take less, 0.02 bn for the last tile's and 1 per wave; the split kernel (N no multiple of 4)
+//   0.1 bn / split for each CTA of an SM.
 // More than two CTAs of the split kernel per SM are not weighed: it does not overlap one tile's outputs with the
 // next one's products, as the pairs do (4096 x 4096 x 256: pair 25.1, split 38.9).
 // Measured, in us, bf16 with residual: 512 x 4096 x 4096 pair, bn 128: 18.6, split, bn 128: 23.5; 256 x 7168 x 2048 pair,
 // bn 128: 12.6, split, bn 128, 2 slices: 17.4; 256 x 2048 x 7168 pair, bn 64: 24.0, split, bn 128, 4 slices: 15.1; 24 x 512
-// x 512 pair: 4.6, split, 8 slices: 4.0; 600 x 3162 x 112 pair 10.7, split 28.5; 600 x 3160 x 112 pair 7.9, split 6.9.
+// x 512 pair: 4.6, split, 8 slices: 4.0; 600 x 3162 x 112 pair 9.9, split 13.4; 600 x 3160 x 112 pair 7.9, split 6.9.
 // Over 238 combinations of sizes and types with N a multiple of 8, and 87 of short K or odd N, the choice is 2.5 % and
-// 3 % off the best of all tiles and slices (geometric mean).
+// 2.1 % off the best of all tiles and slices (geometric mean).
 struct LinearPlan {
     bool pair;
     int bn, split, stages;
@@ -1413,7 +1414,6 @@ int linear_split_stages(int bn, int split, bool own_part, int ctas_per_sm) {
 LinearPlan plan_linear(int sms, long long M, long long N, long long K, bool f8, bool gated, bool residual) {
     const float kStart = 3.9f, kIn = 90e3f;       // us, bytes per us
     const int nk = (int)((K + (f8 ? 127 : 63)) / (f8 ? 128 : 64));
-    const bool odd = N % 8 != 0;                  // rows of y and the residual are stored two bytes at a time
     const float dram = ((gated ? 2 : 1) * (float)N * K * (f8 ? 1 : 2) + (float)M * K * (f8 ? 1 : 2) +
                         (float)M * N * (residual ? 4 : 2)) / 6.4e6f;
     LinearPlan best = {false, 0, 1, 0, 3e38f};
@@ -1423,8 +1423,9 @@ LinearPlan plan_linear(int sms, long long M, long long N, long long K, bool f8, 
         if (bn - (bn > 128 ? 16 : 32) >= M) continue;                 // a smaller tile holds all tokens
         const long long tiles = nt2 * ((M + bn - 1) / bn), waves = (tiles + pairs - 1) / pairs;
         const float kb = linear_pair_stage_bytes(bn) / kIn;
-        const float us = kStart + std::max((float)waves * nk * kb, dram) + 0.2f * waves +
-                         (odd ? 0.02f * bn : 0.0f);
+        float us;
+        if (N % 8 == 0) us = kStart + std::max((float)waves * nk * kb, dram) + 0.2f * waves;
+        else us = kStart + std::max(waves * std::max(nk * kb, 0.037f * bn), dram) + (float)waves + 0.02f * bn;
         if (us < best.us) best = {true, bn, 1, linear_pair_stages(bn), us};
     }
     // K slices over a cluster: 128 weight rows, bn tokens
@@ -1444,7 +1445,7 @@ LinearPlan plan_linear(int sms, long long M, long long N, long long K, bool f8, 
             const int slice = (nk + split - 1) / split;
             const float us = kStart + std::max((float)per_sm * slice * kb, dram) +
                              (split > 1 ? 0.5f + 0.1f * split + 0.026f * bn : 0.0f) +
-                             (odd ? 0.1f * bn * per_sm / split : 0.0f);
+                             (N % 4 ? 0.1f * bn * per_sm / split : 0.0f);
             if (us < best.us) best = {false, bn, split, stages, us};
         }
     }
