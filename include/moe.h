@@ -132,7 +132,7 @@ int moe_route_scored(const moe_bf16* x, const moe_bf16* Wg, const float* bias, c
  * exclusive scan, and a stable permutation of the kept assignments into contiguous
  * per-expert row blocks.
  *   x          [T, d] bf16           hidden states
- *   idx        [T, k] int32          experts per token (distinct within a token, in [0, E))
+ *   idx        [T, k] int32          experts per token (distinct within a token, in [0, E)); -1: dropped
  *   counts_raw [E] int32             assignments per expert before the capacity limit
  *   counts     [E] int32             kept assignments per expert
  *   offsets    [E+1] int32           exclusive scan of counts; offsets[E] = N kept rows
