@@ -197,6 +197,23 @@ def test_nan_and_infinity_stay_in_their_row(moe, M, N, K):
 
 
 @gpu
+@pytest.mark.parametrize("N", [32768, 32771])
+def test_offsets_past_32_bits(moe, N):
+    # more than 2^31 outputs; a residual that repeats every 1000 rows, so the rows checked stand for all
+    M, K = 66001, 64
+    a = inputs(1000, N, K, "silu", True, True)
+    rows = torch.arange(M, device="cuda") % 1000
+    a["x"], a["residual"] = a["x"][rows], a["residual"][rows]
+    y = call(moe, a, "silu")
+    for m0 in (0, 65000, M - 300):
+        part = dict(a, x=a["x"][m0:m0 + 300], residual=a["residual"][m0:m0 + 300])
+        want, tol = define("silu", **wide(part))
+        close(y[m0:m0 + 300], want, tol)
+    for m0 in range(1000, M - 1000, 1000):
+        assert torch.equal(y[m0:m0 + 1000], y[:1000])
+
+
+@gpu
 @pytest.mark.parametrize("M,N,K", [(1, 512, 2048), (33, 100, 512), (2048, 1024, 256), (2050, 1001, 256)])
 def test_residual_in_place_and_repeatable(moe, M, N, K):
     a = inputs(M, N, K, "none", True, True)

@@ -465,3 +465,23 @@ def test_other_stream_and_graph_replay(moe):
     ri, rw = define(other, bias, k, **kw)
     assert np.array_equal(idx.cpu().numpy(), ri)
     np.testing.assert_allclose(w.cpu().numpy(), rw, rtol=1e-5)
+
+
+@gpu
+def test_offsets_past_32_bits(moe):
+    # more than 2^31 logits, all masked but the first and last rows
+    E, k, T = 1024, 2, (1 << 21) + 37
+    kw = dict(n_group=8, topk_group=4, scale=2.5)
+    logits, bias = draw(80, E, 31), draw_bias(E, 31)
+    lg = torch.full((T, E), -np.inf, device="cuda")
+    lg[:40] = torch.from_numpy(logits[:40]).cuda()
+    lg[-40:] = torch.from_numpy(logits[40:]).cuda()
+    idx, w = torch.full((T, k), -7, dtype=torch.int32, device="cuda"), torch.full((T, k), -7.0, device="cuda")
+    p = moe.moe_route_params(n_group=8, topk_group=4, scale=2.5)
+    moe.moe_route_scored(None, None, torch.from_numpy(bias).cuda(), lg, p, T, 64, E, k, None, idx, w, None)
+    torch.cuda.synchronize()
+    assert moe.moe_get_error() == 0
+    ri, rw = define(logits, bias, k, **kw)
+    assert np.array_equal(torch.cat([idx[:40], idx[-40:]]).cpu().numpy(), ri)
+    np.testing.assert_allclose(torch.cat([w[:40], w[-40:]]).cpu().numpy(), rw, rtol=1e-5)
+    assert (idx[40:-40] == -1).all() and (w[40:-40] == 0).all()
