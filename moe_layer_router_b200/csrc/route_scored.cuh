@@ -16,6 +16,8 @@
 // of the keys is the order of the logits, which are compared themselves.
 #pragma once
 
+#include <type_traits>
+
 #include "route_permute_combine.cuh"
 
 namespace moe {
@@ -232,7 +234,7 @@ __device__ __noinline__ void route_token_f64(const RouteScored& p, const RouteLa
 // One warp per token, or two tokens per warp, the experts on the lanes as RouteLanes has them, EPL >= per.  Keys are integers of the floats' order whose
 // last BITS bits hold the position in the lane: a comparison carries the expert along and a lane's keys are distinct.
 //   lanes       sort their four largest keys (8 experts: 32 minima and maxima)
-//   groups      the two largest keys merged over the group's lanes; rank by n_group shuffles
+//   groups      the two largest keys merged over the group's lanes; the topk_group largest of them, one by one
 //   slots       k + 1 times: the largest list head, taken off its lane's list; a lane whose four are used up sorts its
 //               next four
 //   certainty   keys are off by at most route_err and 2^BITS steps.  Neighbours in the order that are closer than that
@@ -368,14 +370,20 @@ route_scored_kernel(const __grid_constant__ RouteScored p, const __grid_constant
         const long long t = t0 + half;
         const float* row = p.logits + t * p.E;
         // ---- keys
-        bool bad = false;
         float top = -INFINITY, total = 1.0f, inv = 1.0f;
+        float zero = 0.0f;                                    // stays 0 while every logit is finite
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            bad |= !(l[i] < INFINITY);
-            l[i] = l[i] < INFINITY ? l[i] : -INFINITY;
+        for (int i = 0; i < EPL; ++i) zero = fmaf(l[i], 0.0f, zero);
+        const bool finite = __all_sync(all, zero == 0.0f);
+        if (!finite) {
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                bad |= !(l[i] < INFINITY);
+                l[i] = l[i] < INFINITY ? l[i] : -INFINITY;
+            }
+            if (__any_sync(all, bad) && threadIdx.x % 32 == 0) record_error(-7 /* MOE_ERR_CHECK */);
         }
-        if (__any_sync(all, bad) && threadIdx.x % 32 == 0) record_error(-7 /* MOE_ERR_CHECK */);
         float ex[EPL];                                        // e^(l - top) or e^-l
         if (KIND == ROUTE_SOFTMAX || (KIND == ROUTE_LOGIT && !p.sigmoid && !p.renorm)) {
 #pragma unroll
@@ -393,24 +401,29 @@ route_scored_kernel(const __grid_constant__ RouteScored p, const __grid_constant
         }
         int key[EPL];
         constexpr int Q = EPL < 4 ? EPL : 4;
+        auto keys = [&](auto masks) {                         // masks: some logits are -inf
 #pragma unroll
-        for (int q = 0; q < EPL; q += Q) {
-            float b4[4];
-            if (!KEEP_BIAS && KIND != ROUTE_LOGIT) {
-                const float4 v = s_bias[(q >> 2) * LPT + lane];
-                b4[0] = v.x; b4[1] = v.y; b4[2] = v.z; b4[3] = v.w;
-            }
-#pragma unroll
-            for (int r = 0; r < Q; ++r) {
-                const int i = q + r;
-                float k32 = l[i];
-                if (KIND != ROUTE_LOGIT) {
-                    const float s = KIND == ROUTE_SIGMOID ? rcp_approx(1.0f + exp_approx(-l[i])) : ex[i] * inv;
-                    k32 = l[i] > -INFINITY ? s + (KEEP_BIAS ? bias[KEEP_BIAS ? i : 0] : b4[r]) : -INFINITY;
+            for (int q = 0; q < EPL; q += Q) {
+                float b4[4];
+                if (!KEEP_BIAS && KIND != ROUTE_LOGIT) {
+                    const float4 v = s_bias[(q >> 2) * LPT + lane];
+                    b4[0] = v.x; b4[1] = v.y; b4[2] = v.z; b4[3] = v.w;
                 }
-                key[i] = (ordered(k32 + 0.0f) & ~POS) | (POS - i);
+#pragma unroll
+                for (int r = 0; r < Q; ++r) {
+                    const int i = q + r;
+                    float k32 = l[i] + 0.0f;                  // no -0 (a sum with a score is none)
+                    if (KIND != ROUTE_LOGIT) {
+                        const float s = KIND == ROUTE_SIGMOID ? rcp_approx(1.0f + exp_approx(-l[i])) : ex[i] * inv;
+                        k32 = s + (KEEP_BIAS ? bias[KEEP_BIAS ? i : 0] : b4[r]);
+                        if (decltype(masks)::value && !(l[i] > -INFINITY)) k32 = -INFINITY;
+                    }
+                    key[i] = (ordered(k32) & ~POS) | (POS - i);
+                }
             }
-        }
+        };
+        if (finite) keys(std::false_type());
+        else keys(std::true_type());
         if (t0 + stride < p.T) load(t + stride);              // on its way while this token is finished
         int head[D];
         largest<EPL, D>(key, 0x7fffffff, head);
