@@ -614,12 +614,13 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                  : "memory");
 }
 
-// One epilogue warp's 32 accumulator lanes of a tile, CH tokens at a time.  The accumulator is read as 8 x 8 fragments (rows: outputs,
-// columns: tokens), finished in registers, and transposed by stmatrix into shared memory as token rows
+// One epilogue warp's 32 accumulator lanes of a tile, CH tokens at a time.  The accumulator is read as 8 x 8
+// fragments (rows: outputs, columns: tokens), finished in registers, and transposed by stmatrix into shared memory as token rows
 // of 64 bytes, from which 16-byte pieces of whole rows go to y; the residual comes in the other way.  Per 8
 // outputs that is 4 conversions, one shared-memory instruction each way and an eighth of a global store; with a lane
 // per output each of these was 8 instructions (16384 x 2048 x 512 with residual, as first built: 61 us this way,
-// 68 us a lane per output, 105 us through fp32 [token][output] in shared memory).  Pieces are XOR-swizzled by row: no bank conflicts.
+// 68 us a lane per output, 105 us through fp32 [token][output] in shared memory).  Pieces are XOR-swizzled
+// by row: no bank conflicts.
 // Rows of y that are not 16-byte aligned (N % 8) are moved an element per lane.
 // GATED: lanes 0-63 of the CTA's accumulator hold x W^T, lanes 64-127 x W_up^T of the same 64 outputs.  The two
 // warps of a pair swap halves of every CH tokens (through the other's buffer, two of them in turn) and each finishes

@@ -455,7 +455,7 @@ int run_route_scored(DeviceInfo* di, const float* logits, int nsplit, float* log
     };
     const RouteLanes warp = lanes(32);
     // two tokens per warp once there are more of them than warps on the GPU at a time (measured: 32768 x 256, 8
-    // groups, 44 us with one, 38 with two)
+    // groups, 44 us with one, 38 with two, as both were first built)
     const bool two = k < 16 && r.n_group <= 16 && lanes(16).per <= 16 && T > 32ll * di->sms;
     const RouteLanes m = two ? lanes(16) : warp;
     const bool vec = nsplit == 1 && m.per % 4 == 0 && each % 4 == 0;

@@ -231,8 +231,8 @@ __device__ __noinline__ void route_token_f64(const RouteScored& p, const RouteLa
 
 // ---------------------------------------------------------------- the kernel: keys in 32 bits
 //
-// One warp per token, or two tokens per warp, the experts on the lanes as RouteLanes has them, EPL >= per.  Keys are integers of the floats' order whose
-// last BITS bits hold the position in the lane: a comparison carries the expert along and a lane's keys are distinct.
+// One warp per token, or two tokens per warp, the experts on the lanes as RouteLanes has them, EPL >= per.
+// Keys are integers of the floats' order whose last BITS bits hold the position in the lane: a comparison carries the expert along and a lane's keys are distinct.
 //   lanes       sort their four largest keys (8 experts: 32 minima and maxima)
 //   groups      the two largest keys merged over the group's lanes; the topk_group largest of them, one by one
 //   slots       k + 1 times: the largest list head, taken off its lane's list; a lane whose four are used up sorts its
@@ -241,7 +241,7 @@ __device__ __noinline__ void route_token_f64(const RouteScored& p, const RouteLa
 //               are put in order by 64-bit keys of the slots alone (one token in 400 for scores of unit variance, 256
 //               experts); where it is the last slot and the key after it, or the last group that stays and the first
 //               that does not, the token is done again in 64 bits (route_token_f64: one in some thousands)
-// Bound by the instructions, about 600 per token at 256 experts in 8 groups (32768 tokens: 38 us), not by the 33.5 MB
+// Bound by the instructions, 555 per token at 256 experts in 8 groups (32768 tokens: 36 us), not by the 33.5 MB
 // of logits (5.2 us at the measured copy rate).
 constexpr int ROUTE_WARPS = 8;
 
