@@ -728,6 +728,7 @@ struct LinearWarp {
                 w.w = up ? z[4 * j + 3] : z[CH / 2 + 4 * j + 3];
                 out[32 * j] = w;
             }
+            __syncwarp();                                     // the barrier takes whole warps
             named_barrier(bar, 64);
 #pragma unroll
             for (int j = 0; j < CH / 8; ++j) {
@@ -945,8 +946,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                     prefetch_l2(p.residual + (long long)(ti.t0 + tok) * p.N + n0 + col);
                 }
             }
-            bool ready = mbar_wait(tfull_bar + acc, acc_phase, abort_flag);
-            if (GATED) ready = named_barrier_all(bar, 64, ready);    // both partners go on, or neither
+            // all lanes leave the wait together: the barrier behind it takes whole warps
+            bool ready = mbar_wait_warp(tfull_bar + acc, acc_phase, abort_flag);
+            if (GATED) {
+                __syncwarp();
+                ready = named_barrier_all(bar, 64, ready);           // both partners go on, or neither
+            }
             if (!__all_sync(0xffffffffu, ready)) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + (uint32_t)(acc * GEMM_ACC_COLS) + ((uint32_t)(sub * 32) << 16);

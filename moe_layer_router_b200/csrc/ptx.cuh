@@ -259,7 +259,8 @@ __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Named barrier over `threads` threads; true where `ok` holds for all of them.
+// Named barrier over `threads` threads of whole warps, whose lanes have to arrive together (.aligned): after a wait or a
+// branch that the lanes can leave one by one, __syncwarp() comes first.  True where `ok` holds for all of them.
 __device__ __forceinline__ bool named_barrier_all(int id, int threads, bool ok) {
     uint32_t r;
     asm volatile(

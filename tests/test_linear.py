@@ -8,6 +8,8 @@ activations have slopes below 1.13 (gelu) and are evaluated to a few ulp: 2^-20 
 gated product carries both factors' errors.  Then one rounding to bf16, at most 2^-8 of the value.
 """
 import math
+import pathlib
+import re
 
 import numpy as np
 import pytest
@@ -136,6 +138,20 @@ def test_definition_gelu_forms_agree_with_their_formulas():
     assert torch.allclose(act64("gelu", z), ref, atol=1e-13)
     tanh = 0.5 * z * (1 + torch.tanh(math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)))
     assert torch.allclose(act64("gelu_tanh", z), tanh, atol=1e-13)
+
+
+def test_warps_arrive_whole_at_aligned_barriers():
+    # an .aligned barrier takes the lanes of a warp together, and a spinning wait lets them go one by one: the
+    # statement in front of each such barrier brings them together, and no wait is taken lane by lane in front of it
+    src = pathlib.Path(__file__).parent.parent / "moe_layer_router_b200" / "csrc" / "linear.cuh"
+    code = [re.sub(r"//.*", "", line).strip() for line in src.read_text().splitlines()]
+    code = [line for line in code if line]
+    at = [i for i, line in enumerate(code) if re.search(r"\bnamed_barrier(_all)?\(", line)]
+    assert len(at) == 2
+    for i in at:
+        assert code[i - 1] == "__syncwarp();", code[i - 1:i + 1]
+    for line in code:       # an answer that is used is the warp's
+        assert not re.search(r"(=|if \(|return) *!?mbar_wait\(", line), line
 
 
 # ----------------------------------------------------------------------------- values (GPU)
