@@ -86,7 +86,7 @@ __device__ __forceinline__ float linear_act(int act, float z) {
         case LIN_SILU: return __fdividef(z, 1.0f + __expf(-z));
         case LIN_GELU: {
             const float q = normal_tail(z);
-            return z < 0.0f ? z * q : fmaf(-z, q, z);
+            return z * (z < 0.0f ? q : 1.0f - q);      // infinity stays: q is 0 there, and z - z q would be NaN
         }
         case LIN_GELU_TANH: return __fdividef(z, 1.0f + __expf(-1.5957691216057308f * fmaf(0.044715f * z * z, z, z)));
         default: return z;

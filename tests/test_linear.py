@@ -213,6 +213,43 @@ def test_nan_and_infinity_stay_in_their_row(moe, M, N, K):
 
 
 @gpu
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,N,K", [(1, 200, 256), (2, 130, 72), (40, 200, 256), (2100, 1000, 256), (2100, 1001, 1032)])
+def test_infinite_pre_activations(moe, M, N, K, act):
+    # an infinity in x makes a whole row of them, of W's signs: what the definition gives for each
+    a = inputs(M, N, K, act, True, True)
+    a["x"][M - 1, 5] = math.inf
+    want, _ = define(act, **wide({n: t[-1:] if n in ("x", "residual") and t is not None else t for n, t in a.items()}))
+    assert not want.isfinite().any() or act == "relu"
+    y = call(moe, a, act)
+    torch.testing.assert_close(y[-1:].double(), want, rtol=2.0 ** -8, atol=0, equal_nan=True)
+    if M > 1:
+        assert y[:-1].isfinite().all()
+
+
+@gpu
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,N,K", [(1, 200, 256), (40, 200, 256), (2100, 1000, 256), (2100, 1001, 1032)])
+def test_sums_past_the_largest_fp32(moe, M, N, K, act):
+    # 2e38 from the product and 3e38 from the bias: an infinity on its way to the activation; without the product, 3e38
+    a = inputs(M, N, K, act, True, False)
+    for n in ("x", "W", "W_up"):
+        if a[n] is not None:
+            a[n].zero_()
+    a["x"][::3, 4] = 2e38
+    a["W"][:, 4] = 1
+    a["bias"].fill_(3e38)
+    if act == "swiglu":
+        a["bias_up"].fill_(0.5)
+    y = call(moe, a, act)
+    over = torch.zeros(M, dtype=torch.bool, device="cuda")
+    over[::3] = True
+    assert (y[over] == math.inf).all()
+    want = torch.tensor(1.5e38 if act == "swiglu" else 3e38, device="cuda").bfloat16()
+    assert (y[~over] == want).all()
+
+
+@gpu
 @pytest.mark.parametrize("N", [32768, 32771])
 def test_offsets_past_32_bits(moe, N):
     # more than 2^31 outputs; a residual that repeats every 1000 rows, so the rows checked stand for all
@@ -325,6 +362,30 @@ def test_fp8_sizes(moe, M, N, K):
 def test_fp8_epilogues(moe, act):
     check8(moe, 70, 200, 192, act, True, True)
     check8(moe, 2048, 264, 256, act, False, True)
+
+
+@gpu
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,N,K", [(1, 200, 64), (40, 200, 64), (2100, 1000, 64), (2100, 1001, 1392)])
+def test_fp8_sums_past_the_largest_fp32(moe, M, N, K, act):
+    # as test_sums_past_the_largest_fp32; the row's code 448 times its scale is 2e38 within a rounding
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    x[::3, 4] = 2e38
+    W = torch.zeros(N, K, device="cuda")
+    W[:, 4] = 1
+    Wq, one = W.to(torch.float8_e4m3fn).view(torch.uint8), torch.ones(N, device="cuda")
+    gated = act == "swiglu"
+    b, bu = torch.full((N,), 3e38, device="cuda"), torch.full((N,), 0.5, device="cuda") if gated else None
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(moe.moe_linear_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    moe.moe_linear_w8a8(x, Wq, one, torch.zeros_like(Wq) if gated else None, one if gated else None, b, bu, None, M, N, K,
+                        getattr(moe, "MOE_ACT_" + act.upper()), y, ws)
+    torch.cuda.synchronize()
+    assert moe.moe_get_error() == 0
+    over = torch.zeros(M, dtype=torch.bool, device="cuda")
+    over[::3] = True
+    assert (y[over] == math.inf).all()
+    assert (y[~over] == torch.tensor(1.5e38 if gated else 3e38, device="cuda").bfloat16()).all()
 
 
 # ----------------------------------------------------------------------------- a block
