@@ -77,18 +77,26 @@ __device__ __forceinline__ float normal_tail(float z) {
     return q * t * __expf(-u * u);
 }
 
+// z / (1 + e^-v), by e^-|v|: the divisor stays within [1, 2], where 1 + e^-v would pass 2^126, from which on its fast
+// reciprocal is 0, while the quotient is still a normal bf16 (z = v = -88: -5e-37).
+__device__ __forceinline__ float times_sigmoid(float z, float v) {
+    const float e = __expf(-fabsf(v));
+    return (v < 0.0f ? z * e : z) * rcp_approx(1.0f + e);
+}
+__device__ __forceinline__ float linear_swiglu(float g, float u) { return times_sigmoid(g, g) * u; }
+
 // Activation of a pre-activation z (not SwiGLU).  gelu: z Phi(z); gelu_tanh: (1 + tanh v) / 2 = sigmoid(2v), so that
-// neither tail cancels.  The fast exponential and divide are a few ulp of fp32 off, far below the bf16 rounding
-// that follows.  relu keeps NaN.
+// neither tail cancels.  The fast exponential of a is off by up to (2 + 1.2 |a|) 2^-23 of its value, the reciprocal by 2^-23:
+// a few ulp near 0, 2^-16 at a = -90, far below the bf16 rounding that follows.  relu keeps NaN.
 __device__ __forceinline__ float linear_act(int act, float z) {
     switch (act) {
         case LIN_RELU: return z < 0.0f ? 0.0f : z;
-        case LIN_SILU: return __fdividef(z, 1.0f + __expf(-z));
+        case LIN_SILU: return times_sigmoid(z, z);
         case LIN_GELU: {
             const float q = normal_tail(z);
             return z * (z < 0.0f ? q : 1.0f - q);      // infinity stays: q is 0 there, and z - z q would be NaN
         }
-        case LIN_GELU_TANH: return __fdividef(z, 1.0f + __expf(-1.5957691216057308f * fmaf(0.044715f * z * z, z, z)));
+        case LIN_GELU_TANH: return times_sigmoid(z, 1.5957691216057308f * fmaf(0.044715f * z * z, z, z));
         default: return z;
     }
 }
@@ -187,7 +195,7 @@ struct LinearCols {
         z[4] += bb.x; z[5] += bb.y; z[6] += bb.z; z[7] += bb.w;
         if (GATED) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[i] = swiglu_f32(z[i], z[i + 4]);
+            for (int i = 0; i < 4; ++i) z[i] = linear_swiglu(z[i], z[i + 4]);
         } else {
             linear_acts(p.act, z);
         }
@@ -252,7 +260,7 @@ __device__ __forceinline__ void linear_join(const LinearParams& p, const float* 
                     b *= sx * wb;
                 }
                 a += ba;
-                a = GATED ? swiglu_f32(a, b + bb) : linear_act(p.act, a);
+                a = GATED ? linear_swiglu(a, b + bb) : linear_act(p.act, a);
                 p.y[(t0 + tok) * p.N + n] = __float2bfloat16_rn(p.residual ? a + res[u] : a);
             }
         }
@@ -544,7 +552,7 @@ linear_rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ W, con
         if (GATED) b += sums[fg * LINR_WK + q][(fr + 2) * MT + fm];
     }
     a += bias;
-    a = GATED ? swiglu_f32(a, b + bias_up) : linear_act(p.act, a);
+    a = GATED ? linear_swiglu(a, b + bias_up) : linear_act(p.act, a);
     p.y[(long long)fm * p.N + fn] = __float2bfloat16_rn(p.residual ? a + res : a);
 }
 
@@ -737,7 +745,7 @@ struct LinearWarp {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float m = up ? z[CH / 2 + 4 * j + e] : z[4 * j + e];
-                    o[4 * j + e] = swiglu_f32(up ? r[e] : m, up ? m : r[e]);
+                    o[4 * j + e] = linear_swiglu(up ? r[e] : m, up ? m : r[e]);
                 }
             }
         } else {

@@ -118,6 +118,13 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
+// 1 / v, off by at most 2^-23 of it; subnormal arguments and results as 0
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // ---------------------------------------------------------------- programmatic dependent launch
 // A kernel launched with programmatic stream serialization may start before the kernel in front of it
 // has ended: grid_wait() returns once that kernel has completed and its writes are visible (at once,

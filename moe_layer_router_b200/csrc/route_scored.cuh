@@ -55,11 +55,6 @@ __device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i ^
 constexpr int ORD_LOWEST = (int)0x80800000;    // ordered(-FLT_MAX): every unmasked key is at least this
 constexpr int ORD_EMPTY = (int)0x80000000;
 
-__device__ __forceinline__ float rcp_approx(float v) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
 // e^x, subnormal results as 0
 __device__ __forceinline__ float exp_approx(float x) {
     float r;

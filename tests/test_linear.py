@@ -197,6 +197,27 @@ def test_far_pre_activations(moe, act):
 
 
 @gpu
+@pytest.mark.parametrize("act,lo,hi", [("silu", -90.0, -60.0), ("swiglu", -90.0, -60.0), ("gelu", -13.0, -8.0),
+                                       ("gelu_tanh", -10.05, -7.0)])
+@pytest.mark.parametrize("M,N,K", [(1, 400, 64), (40, 400, 64), (2100, 1000, 64), (2100, 1001, 64), (2100, 1000, 1032)])
+def test_far_tails_keep_their_values(moe, M, N, K, act, lo, hi):
+    # values down to 1e-38, all of them normal bf16.  The pre-activation is the bias, exact; an exponential of an argument
+    # a is off by at most (2 + 1.2 |a|) 2^-23, forming the argument (two roundings, or three in the cubic) adds 3 |a|
+    # 2^-23, |a| <= 90: (4 + 4.2 * 90) 2^-23 < 2^-14 with the divide; then one rounding to bf16
+    a = inputs(M, N, K, act, True, False)
+    a["x"].zero_()
+    a["bias"] = torch.linspace(lo, hi, N, device="cuda")
+    if act == "swiglu":
+        a["bias_up"].fill_(1.0)
+    want, _ = define(act, **wide({n: t[:1] if n == "x" else t for n, t in a.items()}))
+    assert (want.abs() > 1.2e-38).all()
+    y = call(moe, a, act)
+    assert torch.equal(y, y[:1].expand_as(y))
+    off = ((y[:1].double() - want) / want).abs()
+    assert float(off.max()) <= 2.0 ** -8 + 2.0 ** -13
+
+
+@gpu
 @pytest.mark.parametrize("M,N,K", [(40, 200, 256), (2100, 1000, 256)])
 def test_nan_and_infinity_stay_in_their_row(moe, M, N, K):
     a = inputs(M, N, K, "none", True, True)
