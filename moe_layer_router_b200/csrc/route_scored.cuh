@@ -86,10 +86,12 @@ __device__ __forceinline__ unsigned lanes_ballot(bool v) {
 }
 
 // The weights of the selected experts: lane j < k holds slot j's expert (-1: none) and logit.
-// top / total: the row's largest logit and sum of e^(l - top) over its unmasked experts (softmax
-// without renormalisation).  Renormalised weights are ratios of scores, taken relative to the largest
-// selected one where they would underflow: s_j ~ e^(l_j - m) in softmax, and in sigmoid once all selected
-// logits are below -60.  LPT lanes per token, `lane` among them; warp-collective, writing where `live`.
+// top / total: the row's largest logit and sum of e^(l - top) over its finite logits, those of experts that the bias
+// masks among them (softmax without renormalisation).  Renormalised weights are ratios of scores, which are taken
+// relative to the largest selected one where that is small, so that no score underflows before its ratio does:
+// s_j ~ e^(l_j - m) in softmax; s_j ~ e^(min(l_j, 0) - min(m, 0)) / (1 + e^-|l_j|) in sigmoid.  That exponential is within 2
+// ulp of its rounded argument, and the fast one behind the 1 adds 2 more at most (its error is (2 + 1.2 |l|) 2^-23 of
+// e^-|l|).  LPT lanes per token, `lane` among them; warp-collective, writing where `live`.
 template <int LPT>
 __device__ __forceinline__ void scored_weights(const RouteScored& p, long long t, bool live, int lane, int my_e,
                                                float my_l, float top, float total) {
@@ -104,12 +106,10 @@ __device__ __forceinline__ void scored_weights(const RouteScored& p, long long t
             s = expf(my_l - top) / total;
         }
     } else {
-        if (have) s = rcp_approx(1.0f + exp_approx(-my_l));   // a few ulp
-        if (p.renorm) {
-            const float m = from_ordered(lanes_max<LPT>(ordered(have ? my_l : -INFINITY)));
-            if (have && m < -60.0f) s = expf(my_l - m);       // 1 + e^l is 1
-            s *= rcp_approx(lanes_sum<LPT>(s));
-        }
+        float m = 0.0f;
+        if (p.renorm) m = fminf(from_ordered(lanes_max<LPT>(ordered(have ? my_l : -INFINITY))), 0.0f);
+        if (have) s = expf(fminf(my_l, 0.0f) - m) * rcp_approx(1.0f + exp_approx(-fabsf(my_l)));
+        if (p.renorm) s *= rcp_approx(lanes_sum<LPT>(s));
     }
     if (live && lane < p.k) {
         p.idx[t * p.k + lane] = have ? my_e : -1;

@@ -302,6 +302,21 @@ def test_far_logits(moe, sigmoid):
 
 
 @gpu
+@pytest.mark.parametrize("T", [12, 9000])
+@pytest.mark.parametrize("with_bias", [True, False])
+def test_selected_scores_far_apart(moe, T, with_bias):
+    # renormalised sigmoid weights whose smaller scores underflow in 32 bits while their ratio to the largest does not
+    rows = np.stack([np.linspace(hi, lo, 8) for hi, lo in [(-59, -95), (-50, -88), (-59.99, -87.5), (-30, -110), (0, -87.4),
+                                                           (3, -85), (40, -44), (-60.01, -140), (-86, -104), (-59, -59),
+                                                           (88, -0.5), (-20, -103)]]).astype(np.float32)
+    logits = np.tile(rows, (T // 12, 1))
+    bias = np.zeros(8, np.float32) if with_bias else None
+    for k in (8, 5):
+        idx, w = check(moe, logits, bias, k)
+        assert (w > 0).all()
+
+
+@gpu
 @pytest.mark.parametrize("bad", [np.nan, np.inf])
 @pytest.mark.parametrize("sigmoid", [True, False])
 def test_nan_and_inf_are_reported_and_masked(moe, bad, sigmoid):
