@@ -243,20 +243,26 @@ constexpr int ROUTE_WARPS = 8;
 // Errors in units of 2^-23.  The fast exponential of x is off by at most 2 + 1.16 |x| of its value (x = -l, or
 // l - top in softmax, whose rounding adds |x| / 2), the fast reciprocal by 1, a rounding by 1/2.
 //   sigmoid  the exponential's part reaches s by the factor 1 - s: s (2 + (1 - s) (2 + 1.25 |x|))
-//   softmax  the sum adds its terms' mean error, at most 2 + 1.7 ln E, and its roundings, at most (E / 32 + 5) / 2:
-//            s (40 + 2.5 |x|) for E <= 1024
+//   softmax  the sum has its terms' mean error, at most 2 + 1.66 ln E < 13.6 (the mean of |x| is below the entropy), and
+//            its roundings, a lane's experts and five joins: (EPL + 5) / 2; with the reciprocal, the product and the
+//            exponential's own 2: s (20 + EPL / 2 + 2.5 |x|)
 // and the key's rounding half of |key|.  route_err: of a key whose score and x are known.  route_err_any: of any
 // key with that value: sigmoid, s <= min(1, S) with S = |key| + bmax, and s (1 - s) (2 + 1.25 |x|) < 0.8; softmax,
-// s <= S and s |x| <= s ln(1 / s), which grows with s up to 1 / e.
-__device__ __forceinline__ float route_err(bool sigmoid, float s, float x, float key) {
-    const float rel = sigmoid ? fmaf(1.0f - s, fmaf(1.25f, fabsf(x), 2.0f), 2.0f) : fmaf(2.5f, fabsf(x), 40.0f);
+// s <= S and s |x| <= s ln(1 / s), which grows with s up to 1 / e.  sum: ROUTE_ERR_SUM.
+template <int EPL>
+constexpr float ROUTE_ERR_SUM = 20.0f + 0.5f * EPL;
+
+template <bool SIG>
+__device__ __forceinline__ float route_err(float sum, float s, float x, float key) {
+    const float rel = SIG ? fmaf(1.0f - s, fmaf(1.25f, fabsf(x), 2.0f), 2.0f) : fmaf(2.5f, fabsf(x), sum);
     return 1.1920929e-7f * fmaf(s, rel, fabsf(key)) + 1e-36f;
 }
-__device__ __forceinline__ float route_err_any(bool sigmoid, float key, float bmax) {
+template <bool SIG>
+__device__ __forceinline__ float route_err_any(float sum, float key, float bmax) {
     const float S = fabsf(key) + bmax;
-    if (sigmoid) return 1.1920929e-7f * (2.0f * fminf(S, 1.0f) + 0.8f + fabsf(key));
+    if (SIG) return 1.1920929e-7f * (2.0f * fminf(S, 1.0f) + 0.8f + fabsf(key));
     const float sx = S < 0.36f ? -S * __logf(S + 1e-30f) : 0.37f;
-    return 1.1920929e-7f * (41.0f * S + 2.5f * sx) + 1e-36f;
+    return 1.1920929e-7f * ((sum + 1.0f) * S + 2.5f * sx) + 1e-36f;
 }
 
 __device__ __forceinline__ void order2(int& a, int& b) {      // a >= b
@@ -306,6 +312,7 @@ route_scored_kernel(const __grid_constant__ RouteScored p, const __grid_constant
     constexpr int POS = (1 << BITS) - 1;
     constexpr int D = EPL < 4 ? EPL : 4;
     constexpr float TRUNC = 1.1920929e-7f * (1 << BITS);       // relative, of the position's bits
+    constexpr float SUM = ROUTE_ERR_SUM<EPL>;
     const int lane = threadIdx.x & (LPT - 1), warp = threadIdx.x >> 5, half = (threadIdx.x & 31) / LPT;
     const unsigned all = 0xffffffffu;
     const RouteLane at(p, m, lane);
@@ -457,7 +464,7 @@ route_scored_kernel(const __grid_constant__ RouteScored p, const __grid_constant
                     constexpr bool SIG = KIND == ROUTE_SIGMOID;
                     const float two = p.top2 ? 2.0f : 1.0f, more = p.top2 ? bmax : 0.0f;
                     const float kl = fabsf(fl) + more, kh = fabsf(fh) + more;
-                    sure = fl - fh > two * (route_err_any(SIG, kl, bmax) + route_err_any(SIG, kh, bmax) + TRUNC * (kl + kh)) +
+                    sure = fl - fh > two * (route_err_any<SIG>(SUM, kl, bmax) + route_err_any<SIG>(SUM, kh, bmax) + TRUNC * (kl + kh)) +
                                          2.4e-7f * (fabsf(fl) + fabsf(fh));
                 }
             }
@@ -500,7 +507,7 @@ route_scored_kernel(const __grid_constant__ RouteScored p, const __grid_constant
             const float x = SIG ? my_l : my_l - top;
             const float s = SIG ? rcp_approx(1.0f + exp_approx(-x)) : exp_approx(x) * inv;
             ka = s + (p.bias && entry ? __ldg(p.bias + my_e) : 0.0f);
-            ea = route_err(SIG, s, x, ka);
+            ea = route_err<SIG>(SUM, s, x, ka);
         }
         const float kb = __shfl_down_sync(all, ka, 1), eb = __shfl_down_sync(all, ea, 1);
         const int after = __shfl_down_sync(all, mine, 1);
@@ -509,7 +516,7 @@ route_scored_kernel(const __grid_constant__ RouteScored p, const __grid_constant
             // equal logits of two lanes may have come in the order of their positions
             if (lane + 1 < p.k && after >= ORD_LOWEST) order = ka - kb > ea + eb;
             if (next >= ORD_LOWEST)
-                sure = sure && (KIND == ROUTE_LOGIT ? ka > rest : ka - rest > ea + route_err_any(SIG, rest, bmax));
+                sure = sure && (KIND == ROUTE_LOGIT ? ka > rest : ka - rest > ea + route_err_any<SIG>(SUM, rest, bmax));
         }
         // The slots are the right experts if all are certainly above the rest; otherwise, and where the groups were in
         // doubt, the token is done again.  Their order among themselves is put right here.

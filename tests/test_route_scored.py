@@ -264,6 +264,21 @@ def test_keys_closer_than_a_32_bit_rounding(moe, sigmoid, n_group, topk_group):
 
 
 @gpu
+@pytest.mark.parametrize("E,n_group,topk_group", [(1020, 17, 5), (1023, 31, 31), (1024, 1, 1), (992, 31, 9), (240, 15, 15)])
+@pytest.mark.parametrize("top2", [True, False])
+def test_near_keys_with_many_experts_per_lane(moe, E, n_group, topk_group, top2):
+    # softmax sums of up to 60 terms per lane, and a bias that brings all keys of a row within some 2^-26 of each other (in
+    # every other row: the rows between have other logits)
+    T = 64
+    l = draw(1, E, 51, spread=2.0)
+    e = np.exp(l[0].astype(np.float64) - l[0].max())
+    bias = (0.25 - e / e.sum()).astype(np.float32)
+    logits = l.repeat(T, 0)
+    logits[1::2] += draw(T // 2, E, 52)
+    check(moe, logits, bias, 9, n_group=n_group, topk_group=topk_group, top2=top2, sigmoid=False, renorm=False)
+
+
+@gpu
 @pytest.mark.parametrize("sigmoid", [True, False])
 @pytest.mark.parametrize("n_group,topk_group,top2", [(1, 1, True), (8, 2, True), (8, 2, False), (16, 9, True)])
 @pytest.mark.parametrize("renorm", [True, False])
