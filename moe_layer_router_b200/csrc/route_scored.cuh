@@ -16,6 +16,7 @@
 // of the keys is the order of the logits, which are compared themselves.
 #pragma once
 
+#include <cfloat>
 #include <type_traits>
 
 #include "route_permute_combine.cuh"
@@ -247,8 +248,10 @@ constexpr int ROUTE_WARPS = 8;
 //            its roundings, a lane's experts and five joins: (EPL + 5) / 2; with the reciprocal, the product and the
 //            exponential's own 2: s (20 + EPL / 2 + 2.5 |x|)
 // and the key's rounding half of |key|.  route_err: of a key whose score and x are known.  route_err_any: of any
-// key with that value: sigmoid, s <= min(1, S) with S = |key| + bmax, and s (1 - s) (2 + 1.25 |x|) < 0.8; softmax,
-// s <= S and s |x| <= s ln(1 / s), which grows with s up to 1 / e.  sum: ROUTE_ERR_SUM.
+// key with that value, whose score is at most S = |key| + bmax and at most smax (1; in softmax the largest of the row):
+// sigmoid, s (1 - s) (2 + 1.25 |x|) < 0.8; softmax, s |x| <= s ln(1 / s), which grows with s up to 1 / e.  With smax one
+// large finite bias (an expert switched off by -1e9) leaves the other keys' bounds small.  A bound grows slower than the
+// keys do, so that key + route_err_any(key) bounds every smaller key too.  sum: ROUTE_ERR_SUM.
 template <int EPL>
 constexpr float ROUTE_ERR_SUM = 20.0f + 0.5f * EPL;
 
@@ -258,11 +261,11 @@ __device__ __forceinline__ float route_err(float sum, float s, float x, float ke
     return 1.1920929e-7f * fmaf(s, rel, fabsf(key)) + 1e-36f;
 }
 template <bool SIG>
-__device__ __forceinline__ float route_err_any(float sum, float key, float bmax) {
-    const float S = fabsf(key) + bmax;
-    if (SIG) return 1.1920929e-7f * (2.0f * fminf(S, 1.0f) + 0.8f + fabsf(key));
+__device__ __forceinline__ float route_err_any(float sum, float key, float bmax, float smax) {
+    const float S = fminf(fabsf(key) + bmax, smax);
+    if (SIG) return 1.1920929e-7f * (2.0f * S + 0.8f + fabsf(key));
     const float sx = S < 0.36f ? -S * __logf(S + 1e-30f) : 0.37f;
-    return 1.1920929e-7f * ((sum + 1.0f) * S + 2.5f * sx) + 1e-36f;
+    return 1.1920929e-7f * (fmaf(sum, S, fabsf(key)) + 2.5f * sx) + 1e-36f;
 }
 
 __device__ __forceinline__ void order2(int& a, int& b) {      // a >= b
@@ -401,6 +404,7 @@ route_scored_kernel(const __grid_constant__ RouteScored p, const __grid_constant
             total = lanes_sum<LPT>(part_sum);
             inv = 1.0f / total;
         }
+        const float smax = KIND == ROUTE_SOFTMAX ? inv * 1.0001f : 1.0f;   // no score is above it, errors included
         int key[EPL];
         constexpr int Q = EPL < 4 ? EPL : 4;
         auto keys = [&](auto masks) {                         // masks: some logits are -inf
@@ -438,36 +442,32 @@ route_scored_kernel(const __grid_constant__ RouteScored p, const __grid_constant
                 b = max(max(b, b2), min(a, a2));
                 a = max(a, a2);
             }
-            // the value as an ordered integer (without positions); EMPTY: no expert left
-            int v = a >= ORD_LOWEST ? a & ~POS : ORD_EMPTY;
-            if (p.top2 && b >= ORD_LOWEST)
-                v = max(ORD_LOWEST, ordered(from_ordered(a & ~POS) + from_ordered(b & ~POS) + 0.0f));
-            if (g >= p.n_group) v = ORD_EMPTY;
-            // the topk_group largest, one by one; lo: the last of them, hi: the largest left
+            // the value (without positions) as an ordered integer, and the error of its one or two keys and of their sum;
+            // EMPTY: no expert left.  Largest finite keys may add up to an infinity: clamped
+            const bool both = p.top2 && b >= ORD_LOWEST;
+            const float fa = from_ordered(a & ~POS), fb = both ? from_ordered(b & ~POS) : 0.0f;
+            const float value = fminf(fmaxf(fa + fb, -FLT_MAX), FLT_MAX);
+            int v = g < p.n_group && a >= ORD_LOWEST ? ordered(value + 0.0f) : ORD_EMPTY;
+            float err = 0.0f;                                 // logits are compared as they are
+            if (KIND != ROUTE_LOGIT) {
+                constexpr bool SIG = KIND == ROUTE_SIGMOID;
+                err = route_err_any<SIG>(SUM, fa, bmax, smax) + TRUNC * fabsf(fa) + 2.4e-7f * fabsf(value);
+                if (both) err += route_err_any<SIG>(SUM, fb, bmax, smax) + TRUNC * fabsf(fb);
+            }
+            // the topk_group largest, one by one
             bool kept = false;
-            int lo = ORD_EMPTY;
             for (int q = 0; q < p.topk_group; ++q) {
                 const int most = lanes_max<LPT>(v);
-                lo = most != ORD_EMPTY ? most : lo;
                 const int owner = __ffs(lanes_ballot<LPT>(v == most)) - 1;
                 if (g == (owner >> m.lg) && most != ORD_EMPTY) {
                     kept = true;
                     v = ORD_EMPTY;
                 }
             }
-            const int hi = lanes_max<LPT>(v);
-            if (hi != ORD_EMPTY) {
-                const float fl = from_ordered(lo), fh = from_ordered(hi);
-                if (KIND == ROUTE_LOGIT) {
-                    sure = lo > hi;
-                } else {      // a value is one key, or two of at most |value| + bmax each
-                    constexpr bool SIG = KIND == ROUTE_SIGMOID;
-                    const float two = p.top2 ? 2.0f : 1.0f, more = p.top2 ? bmax : 0.0f;
-                    const float kl = fabsf(fl) + more, kh = fabsf(fh) + more;
-                    sure = fl - fh > two * (route_err_any<SIG>(SUM, kl, bmax) + route_err_any<SIG>(SUM, kh, bmax) + TRUNC * (kl + kh)) +
-                                         2.4e-7f * (fabsf(fl) + fabsf(fh));
-                }
-            }
+            // certain where the least that a kept group can be is above the most that another can be
+            const int most = lanes_max<LPT>(v != ORD_EMPTY ? ordered(value + err) : ORD_EMPTY);
+            const int least = lanes_max<LPT>(kept ? ordered(err - value) : ORD_EMPTY);
+            if (most != ORD_EMPTY) sure = -from_ordered(least) > from_ordered(most);
             if (!kept) {
 #pragma unroll
                 for (int i = 0; i < D; ++i) head[i] = ORD_EMPTY;
@@ -516,7 +516,7 @@ route_scored_kernel(const __grid_constant__ RouteScored p, const __grid_constant
             // equal logits of two lanes may have come in the order of their positions
             if (lane + 1 < p.k && after >= ORD_LOWEST) order = ka - kb > ea + eb;
             if (next >= ORD_LOWEST)
-                sure = sure && (KIND == ROUTE_LOGIT ? ka > rest : ka - rest > ea + route_err_any<SIG>(SUM, rest, bmax));
+                sure = sure && (KIND == ROUTE_LOGIT ? ka > rest : ka - rest > ea + route_err_any<SIG>(SUM, rest, bmax, smax));
         }
         // The slots are the right experts if all are certainly above the rest; otherwise, and where the groups were in
         // doubt, the token is done again.  Their order among themselves is put right here.

@@ -331,6 +331,38 @@ def test_selected_scores_far_apart(moe, T, with_bias):
         assert (w > 0).all()
 
 
+def device_us(moe, logits, bias, k, kw, n=20):      # the least of n calls
+    T, E = logits.shape
+    idx = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, k, device="cuda")
+    lg, b = torch.from_numpy(logits).cuda(), torch.from_numpy(bias).cuda()
+    p = moe.moe_route_params(**kw)
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(n + 1)]
+    for _ in range(3):
+        moe.moe_route_scored(None, None, b, lg, p, T, 64, E, k, None, idx, w, None)
+    for e in ev:
+        e.record()
+        moe.moe_route_scored(None, None, b, lg, p, T, 64, E, k, None, idx, w, None)
+    torch.cuda.synchronize()
+    return min(x.elapsed_time(y) * 1e3 for x, y in zip(ev, ev[1:]))
+
+
+@gpu
+@pytest.mark.parametrize("low", [-1e4, -1e9, float(np.finfo(np.float32).min), 1e4])
+@pytest.mark.parametrize("score,group_score,n_group", [(0, 0, 1), (0, 1, 8), (1, 0, 8), (1, 1, 8)])
+def test_one_large_finite_bias_costs_no_second_pass(moe, low, score, group_score, n_group):
+    # an expert that is switched off (or always on) by a large finite bias, as programs do that have no -inf
+    T, E, k = 16384, 256, 8
+    logits, bias = draw(T, E, 41), draw_bias(E, 41, 0.1 if score else 1.0 / E)
+    kw = dict(score=score, group_score=group_score, n_group=n_group, topk_group=max(1, n_group // 2))
+    plain = device_us(moe, logits, bias, k, kw)
+    bias[77] = low
+    off = device_us(moe, logits, bias, k, kw)
+    assert off < 1.7 * plain, f"{plain:.1f} -> {off:.1f} us"      # a second pass for every token: 2.4 to 3.1 times
+    check(moe, logits[:2000], bias, k, n_group=n_group, topk_group=max(1, n_group // 2), top2=bool(group_score),
+          sigmoid=bool(score))
+
+
 @gpu
 @pytest.mark.parametrize("bad", [np.nan, np.inf])
 @pytest.mark.parametrize("sigmoid", [True, False])
