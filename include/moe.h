@@ -244,7 +244,7 @@ int moe_layer_route_count_scored(const moe_bf16* x, const moe_bf16* Wg, const fl
  *   W_up     [N, K] bf16           MOE_ACT_SWIGLU only, else NULL
  *   bias     [N] fp32 or NULL;     bias_up [N] fp32 or NULL (MOE_ACT_SWIGLU only)
  *   residual [M, N] bf16 or NULL   may be y itself
- *   y        [M, N] bf16           may not overlap x or the weights
+ *   y        [M, N] bf16           may not overlap any other array (MOE_ERR_INVALID_ARG)
  * 1 <= M, N, K <= 2^24, K % 8 == 0; M and N are free.  No workspace: sums that are split over K
  * are joined on chip, in a fixed order.
  */
@@ -259,7 +259,7 @@ int moe_linear(const moe_bf16* x, const moe_bf16* W, const moe_bf16* W_up, const
  * moe_layer_forward_w8()); each row of x is quantised with the scale amax / 448 (as in
  * moe_layer_forward_w8a8()), and the fp32 accumulator is multiplied by both scales before the epilogue.
  *   Wq, Wq_up [N, K] uint8, s, s_up [N] fp32     (the _up pair: MOE_ACT_SWIGLU only, else NULL)
- *   ws holds the codes and scales of x: moe_linear_workspace_bytes(M, K).  K % 16 == 0.
+ *   ws holds the codes and scales of x: moe_linear_workspace_bytes(M, K); it may not overlap any array.  K % 16 == 0.
  */
 int moe_linear_workspace_bytes(int M, int K, size_t* bytes);
 int moe_linear_w8a8(const moe_bf16* x, const uint8_t* Wq, const float* s, const uint8_t* Wq_up, const float* s_up,

@@ -1344,12 +1344,29 @@ int check_linear(const void* x, const void* W, const void* W_up, const float* s,
     const bool gated = act == MOE_ACT_SWIGLU;
     if (gated != (W_up != nullptr) || (f8 && gated != (s_up != nullptr)) || (!gated && bias_up))
         return MOE_ERR_INVALID_ARG;
-    if (static_cast<const void*>(y) == x || static_cast<const void*>(y) == W || static_cast<const void*>(y) == W_up)
-        return MOE_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(W) || !aligned16(W_up) || !aligned16(s) || !aligned16(s_up) || !aligned16(bias) ||
         !aligned16(bias_up) || !aligned16(residual) || !aligned16(y))
         return MOE_ERR_ALIGN;
     return MOE_OK;
+}
+
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return a && b && p < q + b_bytes && q < p + a_bytes;
+}
+
+// What is written, y and the codes at ws, against all that is read: other CTAs may still read it then.  A residual at y
+// itself is read and written element by element, by one thread.
+bool linear_overlaps(const LinearArgs& a, bool f8, const void* ws, size_t ws_bytes) {
+    const size_t M = a.M, N = a.N, K = a.K, w = N * K * (f8 ? 1 : 2), v = N * 4;
+    const struct { const void* p; size_t n; } in[] = {{a.x, M * K * 2}, {a.W, w}, {a.W_up, w}, {a.bias, v}, {a.bias_up, v},
+                                                      {a.sw, v}, {a.sw_up, v}, {a.residual, M * N * 2}};
+    for (const auto& i : in) {
+        if (overlap(ws, ws_bytes, i.p, i.n)) return true;
+        if (i.p != a.residual && overlap(a.y, M * N * 2, i.p, i.n)) return true;
+    }
+    return overlap(a.y, M * N * 2, ws, ws_bytes) ||
+           (a.residual != a.y && overlap(a.y, M * N * 2, a.residual, M * N * 2));
 }
 
 LinearParams linear_params(const LinearArgs& a) {
@@ -1590,9 +1607,10 @@ int moe_linear(const moe_bf16* x, const moe_bf16* W, const moe_bf16* W_up, const
                const moe_bf16* residual, int M, int N, int K, int act, moe_bf16* y, moe_stream_t stream) {
     int rc = check_linear(x, W, W_up, nullptr, nullptr, false, bias, bias_up, residual, M, N, K, act, y);
     if (rc != MOE_OK) return rc;
+    const LinearArgs a = {x, W, W_up, nullptr, nullptr, nullptr, bias, bias_up, residual, M, N, K, act, y};
+    MOE_REQUIRE(!linear_overlaps(a, false, nullptr, 0), MOE_ERR_INVALID_ARG);
     DeviceInfo* di;
     if ((rc = device_info(&di)) != MOE_OK) return rc;
-    const LinearArgs a = {x, W, W_up, nullptr, nullptr, nullptr, bias, bias_up, residual, M, N, K, act, y};
     return run_linear<false>(di, a, static_cast<cudaStream_t>(stream));
 }
 
@@ -1613,12 +1631,13 @@ int moe_linear_w8a8(const moe_bf16* x, const uint8_t* Wq, const float* s, const 
     size_t need = 0;
     moe_linear_workspace_bytes(M, K, &need);
     MOE_REQUIRE(ws_bytes >= need, MOE_ERR_WORKSPACE);
-    DeviceInfo* di;
-    if ((rc = device_info(&di)) != MOE_OK) return rc;
     uint8_t* xq = static_cast<uint8_t*>(ws);
     float* sx = reinterpret_cast<float*>(xq + linear_scale_offset(M, K));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     LinearArgs a = {x, Wq, Wq_up, sx, s, s_up, bias, bias_up, residual, M, N, K, act, y};
+    MOE_REQUIRE(!linear_overlaps(a, true, ws, need), MOE_ERR_INVALID_ARG);
+    DeviceInfo* di;
+    if ((rc = device_info(&di)) != MOE_OK) return rc;
     if ((rc = quant_linear_x(a, xq, sx, st)) != MOE_OK) return rc;
     a = {xq, Wq, Wq_up, sx, s, s_up, bias, bias_up, residual, M, N, K, act, y};
     return run_linear<true>(di, a, st);

@@ -132,6 +132,24 @@ def test_refusals(moe):
         moe.moe_linear_w8a8(16, host, 32, None, None, None, None, None, 8, 64, 64, 0, 64, 128, stream=0)
 
 
+def test_overlapping_arrays_are_refused(moe):
+    L = moe.lib()
+    def lin(x, W, y, act=0, up=None, b=None, bu=None, r=None):
+        return L.moe_linear(x, W, up, b, bu, r, 8, 64, 64, act, y, None)
+    # 8 x 64 outputs are 1024 bytes at y, x as many, the weights 8192 (fp8: 4096), a bias or scales 256
+    far = dict(x=1 << 20, W=2 << 20, y=3 << 20)
+    top = far["y"] + 1024
+    for kw in [dict(x=top - 16), dict(x=far["y"] - 1008), dict(W=top - 16), dict(W=far["y"] - 8176), dict(r=far["y"] + 128),
+               dict(r=far["y"] - 128), dict(b=far["y"] - 240), dict(b=top - 16),
+               dict(act=5, up=far["y"] - 16), dict(act=5, up=4 << 20, bu=far["y"])]:
+        assert lin(**{**far, **kw}) == -1, kw
+    def lin8_at(ws=5 << 20, x=1 << 20, W=2 << 20, s=6 << 20, y=3 << 20, r=None, b=None):
+        return L.moe_linear_w8a8(x, W, s, None, None, b, None, r, 8, 64, 64, 0, y, ws, 1 << 20, None)
+    for kw in [dict(ws=(1 << 20) + 512), dict(ws=(2 << 20) + 4080), dict(ws=6 << 20), dict(ws=(3 << 20) - 528),
+               dict(ws=3 << 20), dict(r=5 << 20), dict(b=(5 << 20) + 512), dict(s=(3 << 20) + 1008), dict(r=(3 << 20) + 16)]:
+        assert lin8_at(**kw) == -1, kw
+
+
 def test_definition_gelu_forms_agree_with_their_formulas():
     z = torch.linspace(-9, 9, 101, dtype=torch.float64)
     ref = torch.tensor([v * 0.5 * (1 + math.erf(v / math.sqrt(2))) for v in z.tolist()], dtype=torch.float64)
@@ -297,6 +315,20 @@ def test_residual_in_place_and_repeatable(moe, M, N, K):
     inplace = a["residual"].clone()
     moe.moe_linear(a["x"], a["W"], None, a["bias"], None, inplace, M, N, K, 0, inplace)
     assert torch.equal(inplace, y)
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(1, 64, 64), (40, 200, 256), (2100, 1000, 256)])
+def test_arrays_side_by_side(moe, M, N, K):
+    # y between its inputs, without a gap
+    a = inputs(M, N, K, "silu", True, True)
+    want = call(moe, a, "silu")
+    parts = [a["x"], a["W"], torch.zeros(M, N, dtype=torch.bfloat16, device="cuda"), a["residual"]]
+    arena = torch.cat([p.flatten() for p in parts])
+    x, W, y, r = (v.view(p.shape) for v, p in zip(arena.split([p.numel() for p in parts]), parts))
+    moe.moe_linear(x, W, None, a["bias"], None, r, M, N, K, moe.MOE_ACT_SILU, y)
+    assert torch.equal(y, want)
+    assert torch.equal(x, a["x"]) and torch.equal(W, a["W"]) and torch.equal(r, a["residual"])
 
 
 @gpu
