@@ -364,6 +364,44 @@ def test_other_stream_graph_and_two_calls_at_once(moe):
     assert torch.equal(outs[0], want[1])
 
 
+@gpu
+def test_captured_fork_and_join(moe):
+    # two branches of a captured graph, each a chain of dependent calls, joined by a third
+    M, d, f = 24, 512, 1024
+    a, b = inputs(M, f, d, "silu", True, False), inputs(M, f, d, "swiglu", False, False, seed=1)
+    c = inputs(M, d, f, "none", False, True)
+    h, g, y = (torch.empty(M, n, dtype=torch.bfloat16, device="cuda") for n in (f, f, d))
+
+    def first(stream=None):
+        moe.moe_linear(a["x"], a["W"], None, a["bias"], None, None, M, f, d, moe.MOE_ACT_SILU, h, stream=stream)
+        moe.moe_linear(h, c["W"], None, None, None, None, M, d, f, moe.MOE_ACT_NONE, y, stream=stream)
+
+    def second(stream=None):
+        moe.moe_linear(b["x"], b["W"], b["W_up"], None, None, None, M, f, d, moe.MOE_ACT_SWIGLU, g, stream=stream)
+
+    def last():
+        moe.moe_linear(g, c["W"], None, None, None, y, M, d, f, moe.MOE_ACT_NONE, y)
+
+    first(), second(), last()
+    torch.cuda.synchronize()
+    want = y.clone()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        second(side)
+        first()
+        main.wait_stream(side)
+        last()
+    for t in (h, g, y):
+        t.zero_()
+    for _ in range(5):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+    assert moe.moe_get_error() == 0
+
+
 # ----------------------------------------------------------------------------- fp8
 
 def rows_to_e4m3(x):
@@ -439,6 +477,80 @@ def test_fp8_sums_past_the_largest_fp32(moe, M, N, K, act):
     over[::3] = True
     assert (y[over] == math.inf).all()
     assert (y[~over] == torch.tensor(1.5e38 if gated else 3e38, device="cuda").bfloat16()).all()
+
+
+# ----------------------------------------------------------------------------- the kernel that a size runs on
+
+def plan(M, N, K, f8, gated, residual=True, sms=148):
+    """(kernel, tokens per tile, K slices, waves): plan_linear() of moe_api.cu again, so that what the sizes below reach
+    is known."""
+    if M <= 2 and not f8:
+        return "rows", M, 1, 1
+    nk = -(-K // (128 if f8 else 64))
+    dram = ((2 if gated else 1) * N * K * (1 if f8 else 2) + M * K * (1 if f8 else 2) + M * N * (4 if residual else 2)) / 6.4e6
+    found = []
+    nt, bn = -(-N // (128 if gated else 256)), 256
+    while bn >= 32:
+        step = 16 if bn > 128 else 32
+        if bn - step < M:
+            waves, kb = -(-nt * -(-M // bn) // (sms // 2)), (128 * 128 + bn // 2 * 128) / 90e3
+            us = 3.9 + max(waves * nk * kb, dram) + 0.2 * waves
+            if N % 8:
+                us = 3.9 + max(waves * max(nk * kb, 0.037 * bn), dram) + waves + 0.02 * bn
+            found.append((us, "16 warps" if nk <= 10 else "8 warps", bn, 1, waves))
+        bn -= step
+    nt = -(-N // (64 if gated else 128))
+    for want in (128, 64):
+        mt = -(-M // want)
+        bn = (-(-M // mt) + 15) // 16 * 16
+        tiles = nt * -(-M // bn)
+        for split in (1, 2, 4, 8):
+            per = -(-tiles * split // sms)
+            if split > nk or per > 2:
+                break
+            us = 3.9 + max(per * -(-nk // split) * (128 * 128 + 128 * bn) / 90e3, dram)
+            us += 0.5 + 0.1 * split + 0.026 * bn if split > 1 else 0
+            us += 0.1 * bn * per / split if N % 4 else 0
+            found.append((us, "split", bn, split, 1))
+    return min(found, key=lambda c: c[0])[1:]
+
+
+LARGE = [(4099, 4104, 2064), (4099, 4101, 2064)]      # persistent pairs over several tiles, K long
+LARGE_SHORT = [(4099, 4104, 528), (4099, 4101, 528)]  # and K short
+SPLIT = [(3, 4096, 7168), (8, 7168, 4096), (128, 2048, 4096), (128, 4096, 4096), (256, 1000, 4096), (256, 2048, 7168),
+         (256, 4096, 7168), (256, 1000, 2048), (40, 2050, 7168), (130, 2049, 4112), (33, 2052, 2064), (5, 100, 4096),
+         (3, 2048, 4096), (3, 1000, 4096), (200, 300, 7168), (128, 2048, 7168),
+         (256, 200, 7168)]
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("f8", [False, True])
+def test_sizes_reach_every_kernel(f8, gated):
+    for (M, N, K), warps in [(s, "8 warps") for s in LARGE] + [(s, "16 warps") for s in LARGE_SHORT]:
+        kernel, bn, _, waves = plan(M, N, K, f8, gated)
+        assert kernel == warps and bn > 96 and waves >= 3, (M, N, K, kernel, bn, waves)
+        # whatever the estimate: more than two split CTAs per SM are not weighed, and K alone decides the warps
+        assert -(-N // 128) * -(-M // 128) > 2 * 148 and (-(-K // (128 if f8 else 64)) > 10) == (warps == "8 warps")
+    plans = [plan(*s, f8, gated) for s in SPLIT]
+    for split in (2, 4, 8):       # up to 32 tokens per tile the partial sums have memory of their own
+        for few in (True, False):
+            assert any(p[0] == "split" and p[2] == split and (p[1] <= 32) == few for p in plans), (split, few, plans)
+
+
+@gpu
+@pytest.mark.parametrize("act", ["none", "gelu", "swiglu"])
+@pytest.mark.parametrize("M,N,K", LARGE + LARGE_SHORT)
+def test_pairs_over_several_tiles(moe, M, N, K, act):
+    check(moe, M, N, K, act, bias=True, residual=True)
+    check8(moe, M, N, K, act, bias=True, residual=True, zero_row=True)
+
+
+@gpu
+@pytest.mark.parametrize("act", ["silu", "swiglu"])
+@pytest.mark.parametrize("M,N,K", SPLIT)
+def test_sums_cut_over_a_cluster(moe, M, N, K, act):
+    check(moe, M, N, K, act, bias=True, residual=True)
+    check8(moe, M, N, K, act, bias=True, residual=True, zero_row=True)
 
 
 # ----------------------------------------------------------------------------- a block

@@ -479,6 +479,64 @@ def test_fp8_layer(moe, a8):
 
 
 @gpu
+@pytest.mark.parametrize("exchange", ["put", "fused", "a2a"])
+@pytest.mark.parametrize("cap_mode", [0, 1])
+@pytest.mark.parametrize("masked", [False, True])
+def test_scored_routing_goes_on_into_the_sharded_and_the_expert_parallel_layer(moe, exchange, cap_mode, masked):
+    # from moe_layer_route_count_scored on as from moe_layer_route_count, against the whole batch in one call, bit for bit;
+    # masked: most experts switched off, so that every token has slots that no expert is left for
+    from moe_layer_router_b200.ep import EmulatedEP
+    R, T, d, E, k, f, fs = 2, 96, 256, 16, 4, 192, 128
+    a = layer_inputs(R * T, d, E, f, fs, seed=23)
+    bias = draw_bias(E, 24)
+    if masked:
+        bias[[0, 1, 2, 5, 6, 7, 8, 9, 10, 12, 14]] = -np.inf
+    bias = torch.from_numpy(bias).cuda()
+    p = moe.moe_route_params(n_group=4, topk_group=2, scale=2.5)
+    C = moe.moe_capacity(R * T, E, k, 1.25, cap_mode)
+    whole = torch.empty(R * T, d, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(moe.moe_workspace_bytes(R * T, d, E, k, f, fs), dtype=torch.uint8, device="cuda")
+    moe.moe_layer_forward_scored(a["x"], a["Wg"], bias, p, *a["W"], *a["Ws"], fs, R * T, d, E, k, f, 1.25, cap_mode, whole,
+                                 ws)
+    LW = moe.moe_workspace_layout(R * T, d, E, k, f, fs)
+    idx = moe.workspace_view(ws, LW, "idx", (R * T, k), torch.int32)
+    dest = moe.workspace_view(ws, LW, "dest", (R * T, k), torch.int32)
+    assert bool((idx == -1).any(1).all()) == masked and (dest[idx == -1] == -1).all()
+    if cap_mode:
+        assert bool((dest[idx != -1] == -1).any())                        # capacity drops slots too
+    x = [a["x"][r * T:(r + 1) * T].contiguous() for r in range(R)]
+    # token-sharded
+    L = moe.moe_workspace_layout(T, d, E, k, f, fs)
+    parts = [torch.empty(moe.moe_workspace_bytes(T, d, E, k, f, fs), dtype=torch.uint8, device="cuda") for _ in range(R)]
+    for r in range(R):
+        moe.moe_layer_route_count_scored(x[r], a["Wg"], bias, p, fs, T, d, E, k, f, parts[r])
+    counts = torch.stack([moe.workspace_view(w, L, "counts_raw", (E,), torch.int32) for w in parts])
+    out = [torch.empty(T, d, dtype=torch.bfloat16, device="cuda") for _ in range(R)]
+    for r in range(R):
+        base = torch.empty(E, dtype=torch.int32, device="cuda")
+        moe.moe_fill_base(counts, R, r, E, base)
+        moe.moe_layer_finish(x[r], *a["W"], *a["Ws"], fs, T, d, E, k, f, C, base, out[r], parts[r])
+    assert torch.equal(torch.cat(out), whole)
+
+    # expert-parallel, its routing step replaced
+    class Scored:
+        def __getattr__(self, name):
+            return getattr(moe, name)
+
+        def moe_layer_route_count(self, x, Wg, bias, *rest):
+            moe.moe_layer_route_count_scored(x, Wg, bias, p, *rest)
+
+    ep = EmulatedEP(R, T, d, E, k, f, fs, exchange=exchange)
+    ep.moe = Scored()
+    for o in out:
+        o.zero_()
+    ep.forward(x, a["Wg"], bias, *a["W"], *a["Ws"], 1.25, cap_mode, out)
+    torch.cuda.synchronize()
+    assert torch.equal(torch.cat(out), whole)
+    assert moe.moe_get_error() == 0
+
+
+@gpu
 def test_padded_tokens_drop_out_of_the_layer(moe):
     # logits of -inf from a masked batch: the permutation drops the rows, the combine leaves them zero
     T, d, E, k, f, live = 96, 256, 16, 4, 128, 61
