@@ -441,7 +441,10 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
 // of a block along K (with 1, 2, 4, 8 of them one token takes 10.4, 8.6, 8.7, 8.7 us at 4096 x 4096, 25.2, 22.1, 20.4,
 // 20.8 us at 14336 x 4096 and 15.1, 9.2, 7.4, 8.3 us at 2048 x 7168).  No tensor memory, no ring, no cluster:
 // linear_split_kernel, whose tile has to be set up, drained and joined around the loads, takes 11.4, 22.7 and
-// 10.6 us for these.
+// 10.6 us for these.  Narrow layers too are faster here, though N / 8 blocks leave SMs idle where the other cuts K over a
+// cluster; in us, here and there, weights in L2: one token 64 x 14336 6.0, 9.8; 512 x 7168 4.0, 7.2; 1024 x 1024 2.1, 4.7; two
+// tokens 64 x 14336 6.4, 9.8; SwiGLU, one token, 512 x 7168 4.4, 7.2.  It loses by 1 to 3 % for SwiGLU at 2048 x 7168 and by
+// 11 % for two tokens at 14336 x 4096 (23.8, 21.4).
 constexpr int LINR_THREADS = 256;
 constexpr int LINR_MAX_TOKENS = 2;
 constexpr int LINR_WK = 4;                          // warps along K

@@ -237,8 +237,14 @@ __device__ __noinline__ void route_token_f64(const RouteScored& p, const RouteLa
 //               are put in order by 64-bit keys of the slots alone (one token in 400 for scores of unit variance, 256
 //               experts); where it is the last slot and the key after it, or the last group that stays and the first
 //               that does not, the token is done again in 64 bits (route_token_f64: one in some thousands)
-// Bound by the instructions, 555 per token at 256 experts in 8 groups (32768 tokens: 36 us), not by the 33.5 MB
-// of logits (5.2 us at the measured copy rate).
+// Bound by what a token's steps wait for, not by the 33.5 MB of logits (5.2 us at the measured copy rate), nor by the
+// instruction rate alone: 32768 tokens of 256 experts in 8 groups take 36 us, their 18.3 M warp instructions (557 a token) 16
+// at one per cycle.  Each round of the groups and of the slots is a maximum over the lanes, a ballot and a shift, every one of
+// which needs the one before it.  At 24 warps per SM an instruction issues in 59 % of the cycles; per issue, warps wait 2.2
+// cycles for shuffles and the special functions, 2.2 for fixed latencies, 1.2 for memory, 0.8 for the integer pipe, which half
+// of the instructions use.  A few thousand tokens are one per warp: one token's latency (4099 x 160: 7.8 us).
+// 39 of the 48 kernels keep 4 to 172 bytes per thread on the stack under the launch bounds below, where more blocks with fewer
+// registers gave nothing or lost 8 %.
 constexpr int ROUTE_WARPS = 8;
 
 // Errors in units of 2^-23.  The fast exponential of x is off by at most 2 + 1.16 |x| of its value (x = -l, or
